@@ -85,7 +85,10 @@ typedef enum {
   PTL_ERR_TIMEOUT = 8,     /* a bounded device-side wait ran out (kernel returned early) */
   PTL_ERR_UNSUPPORTED = 9, /* no sm_100 device, or a feature not built */
   PTL_ERR_BAD_MASK = 10,   /* attention mask out of range (ptl_attention_masked) */
-  PTL_ERR_BAD_IDS = 11     /* embedding id outside its table or bad bag offsets (ptl_rep_encoder) */
+  PTL_ERR_BAD_IDS = 11,    /* embedding id outside its table or bad bag offsets (ptl_rep_encoder) */
+  PTL_ERR_BAD_PAGE = 12,   /* a page number outside the cache, or positions outside the page table */
+  PTL_ERR_CACHE_FULL = 13, /* not enough free pages (ptl_kv_pool_*) */
+  PTL_ERR_NO_MEMORY = 14   /* a host allocation failed (ptl_kv_pool_*) */
 } ptl_status;
 
 typedef enum { PTL_F32 = 0, PTL_BF16 = 1 } ptl_dtype;
@@ -255,6 +258,8 @@ typedef enum {
   PTL_KERNEL_HEAD = 10,        /* prediction head + compaction */
   PTL_KERNEL_COPY = 11,        /* debug-output copies */
   PTL_KERNEL_COMBINE = 12,     /* weighted top-2 combine + residual */
+  PTL_KERNEL_KV_APPEND = 13,   /* new tokens into the paged cache */
+  PTL_KERNEL_KV_COPY = 14,     /* page copies of the paged cache */
   PTL_KERNEL_END = 99
 } ptl_kernel_kind;
 
@@ -447,6 +452,127 @@ ptl_status ptl_linear_fp8(const uint8_t* xq, const float* sx, const uint8_t* wq,
  * num_parts < 1. */
 ptl_status ptl_partition_users(const int32_t* cu_seqlens, int32_t num_users, int32_t num_parts,
                                int32_t* user_begin);
+
+/* ---- The 8-bit paged key/value cache. ----
+ * A served user's history need not be computed again for each request: its
+ * keys and values are kept in pages, quantised to e4m3, and only the new
+ * tokens (the next action, or the candidates to score) run through the layer.
+ * One layer of a served batch is then ptl_qkv_projection, ptl_kv_append,
+ * ptl_attention_paged, ptl_out_projection, ptl_gate, ptl_moe, with one
+ * ptl_kv_pages per layer and one page table for all layers.
+ *
+ * Layout.  A page holds PTL_KV_PAGE = 64 consecutive tokens of one sequence:
+ *   codes  uint8 [num_pages][2][8][64][64]: [0] keys as [head][token][dim],
+ *          [1] values as [head][dim][token], e4m3 (largest finite 448),
+ *   scales float [num_pages][2][8], one per page, side and head, always a
+ *          power of two, at least 2^-100; a code stands for code * scale.
+ * page_table: device int32 [U][max_pages]; entry k of user u is the page of
+ * tokens 64 k .. 64 k + 63 of its sequence.  past_lens: device int32 [U], the
+ * tokens of user u's sequence before this call; token i of user u in the call
+ * stands at position past_lens[u] + i.  The tables belong to the caller;
+ * ptl_kv_pool_* keeps them for it.  max_pages: 1 .. 2^25 - 1.
+ *
+ * ptl_kv_append writes the keys and values of qkv[T][1536] (columns 512..1535)
+ * at their positions.  A touched page and side and head gets the scale
+ *   s = the smallest power of two with max |x| <= 448 s over its new tokens,
+ * not below the scale it has if the page keeps tokens (those before
+ * past_lens[u]), and the codes e4m3(x / s), to nearest even; where the scale
+ * rises, the kept tokens' codes become e4m3(code * old / s), which loses
+ * nothing but bits that fall below e4m3's smallest step.  Infinities and NaN
+ * are stored as NaN and do not count for the scale.  A page whose first token
+ * is new is written whole, zeros behind the tokens; elsewhere bytes behind the
+ * last token stay as they are.  Positions may be written again (tokens taken
+ * back, then others appended).  A page must not be written for two users in
+ * one call, and not while another sequence shares it: its contents are then
+ * undefined.  workspace: at least 256 bytes (the error word).
+ *
+ * ptl_attention_paged computes softmax(Q K^T / 8) V for the new tokens, Q from
+ * qkv (columns 0..511), keys and values from the pages, which hold the new
+ * tokens too (append first).  The query at position i sees key j iff j <= i
+ * and, when window > 0, i - j < window or j < sinks: a sliding window whose
+ * sequence's first `sinks` tokens stay visible.  Every query sees itself.
+ * window <= 0: no window, sinks unused.  Only the pages that some query sees
+ * are read; what masked positions hold, NaN included, has no effect.  Two
+ * users of a call may name the same pages.  attn: [T][512] in dt.
+ * PTL_ERR_BAD_MASK for sinks < 0.  workspace:
+ * ptl_attention_paged_workspace_size(T, U, dt) bytes.
+ *
+ * Device checks of both: cu_seqlens as everywhere; past_lens[u] < 0 or
+ * past_lens[u] + n > 64 max_pages set PTL_ERR_BAD_PAGE, and in either case
+ * nothing is written; a page number outside 0 .. num_pages - 1 that is needed
+ * sets PTL_ERR_BAD_PAGE (the append skips that page, the attention's output
+ * is undefined).
+ *
+ * ptl_kv_copy_pages: page dst[i] = page src[i], codes and scales, for device
+ * int32 src, dst [count] (the lists that ptl_kv_pool_fork and
+ * ptl_kv_pool_compact give).  A page may be copied to several, but a
+ * destination must appear once and be no source (its contents are otherwise
+ * undefined).  A page number out of range sets PTL_ERR_BAD_PAGE and that copy
+ * is skipped.  workspace: at least 256 bytes. */
+#define PTL_KV_PAGE 64
+#define PTL_KV_PAGE_BYTES 65536
+typedef struct {
+  uint8_t* codes;    /* device [num_pages][2][8][64][64], 16-byte aligned */
+  float* scales;     /* device [num_pages][2][8] */
+  int32_t num_pages; /* >= 1 */
+} ptl_kv_pages;
+ptl_status ptl_kv_append(const void* qkv, const int32_t* cu_seqlens, int32_t num_users, int64_t total_tokens,
+                         ptl_dtype dt, const ptl_kv_pages* kv, const int32_t* page_table, int32_t max_pages,
+                         const int32_t* past_lens, void* workspace, size_t ws_bytes, void* stream);
+size_t ptl_attention_paged_workspace_size(int64_t max_tokens, int32_t max_users, ptl_dtype dt);
+ptl_status ptl_attention_paged(const void* qkv, void* attn, const int32_t* cu_seqlens, int32_t num_users,
+                               int64_t total_tokens, ptl_dtype dt, const ptl_kv_pages* kv, const int32_t* page_table,
+                               int32_t max_pages, const int32_t* past_lens, int32_t window, int32_t sinks,
+                               void* workspace, size_t ws_bytes, void* stream);
+ptl_status ptl_kv_copy_pages(const ptl_kv_pages* kv, const int32_t* src, const int32_t* dst, int64_t count,
+                             void* workspace, size_t ws_bytes, void* stream);
+
+/* Whose pages are whose: a host object (no GPU work, no device memory) that
+ * keeps the page lists of num_seqs sequences over num_pages pages.  Pages are
+ * handed out lowest number first.  A page whose 64 tokens are all written may
+ * be shared by several sequences (counted); the page that a sequence is still
+ * filling never is.  Every call either does all it is asked or, with a status
+ * other than PTL_OK, nothing.  Calls on one pool must not overlap in time.
+ * Kernels issued for an earlier table are not affected by later calls as long
+ * as everything runs in order on one stream.
+ *   create     PTL_ERR_SHAPE for num_pages < 1 or num_seqs < 1.
+ *   reserve    makes room for seqs[i] to hold new_lens[i] tokens (not fewer
+ *              than it holds; the same sequence may appear once) and sets its
+ *              length; PTL_ERR_CACHE_FULL if the pages do not suffice.
+ *   fork       dst[i], which must be empty and appear once, becomes a copy of
+ *              src[i]: full pages are shared; an unfinished last page gets a
+ *              page of its own, and the pair to copy is written to
+ *              copy_src / copy_dst (room for n entries; *n_copies written).
+ *              A src may appear several times but must not be a dst.
+ *   release    empties sequences; pages that none holds any more are free.
+ *   trim       gives up the pages that no later token of the sequence can see
+ *              with this window and these sinks (window >= 1): those that end
+ *              before position length - window + 1 and start at or behind
+ *              `sinks`.  Their table entries become -1.  *freed (nullable)
+ *              receives how many pages became free.
+ *   compact    moves pages down so that pages 0 .. (used - 1) are the ones in
+ *              use, and writes the moves (sources all >= used, destinations all
+ *              below) to copy_src / copy_dst; PTL_ERR_SHAPE, with *n_copies =
+ *              the moves it would take, if capacity is smaller than that.
+ *   table      writes rows of a page table for seqs[0 .. n-1], -1 behind each
+ *              list; PTL_ERR_SHAPE if max_pages is smaller than a list.
+ *   length     tokens of a sequence (-1 for a bad number); free_pages likewise.
+ * Sequence numbers out of 0 .. num_seqs - 1 give PTL_ERR_SHAPE. */
+typedef struct ptl_kv_pool ptl_kv_pool;
+ptl_status ptl_kv_pool_create(int32_t num_pages, int32_t num_seqs, ptl_kv_pool** pool);
+void ptl_kv_pool_destroy(ptl_kv_pool* pool);
+ptl_status ptl_kv_pool_reserve(ptl_kv_pool* pool, const int32_t* seqs, const int32_t* new_lens, int32_t n);
+ptl_status ptl_kv_pool_fork(ptl_kv_pool* pool, const int32_t* src, const int32_t* dst, int32_t n, int32_t* copy_src,
+                            int32_t* copy_dst, int32_t* n_copies);
+ptl_status ptl_kv_pool_release(ptl_kv_pool* pool, const int32_t* seqs, int32_t n);
+ptl_status ptl_kv_pool_trim(ptl_kv_pool* pool, const int32_t* seqs, int32_t n, int32_t window, int32_t sinks,
+                            int32_t* freed);
+ptl_status ptl_kv_pool_compact(ptl_kv_pool* pool, int32_t capacity, int32_t* copy_src, int32_t* copy_dst,
+                               int32_t* n_copies);
+ptl_status ptl_kv_pool_table(const ptl_kv_pool* pool, const int32_t* seqs, int32_t n, int32_t max_pages,
+                             int32_t* table);
+int32_t ptl_kv_pool_length(const ptl_kv_pool* pool, int32_t seq);
+int32_t ptl_kv_pool_free_pages(const ptl_kv_pool* pool);
 
 /* ---- Failure detection self-test. ----
  * Every wait inside the library's kernels (on an mbarrier phase, or on a

@@ -338,6 +338,100 @@ def linear_fp8(x, weight, bias=None, precision=None):
 
 
 # --------------------------------------------------------------------------
+# The 8-bit paged key/value cache (no counterpart in the pages' text beyond the
+# paged cache that the recsys README lists; the layout is this library's)
+# --------------------------------------------------------------------------
+KV_PAGE = 64
+
+
+def kv_scale(amax):
+    """The smallest power of two s with amax <= 448 s, at least 2^-100."""
+    k = -100
+    while 448.0 * 2.0 ** k < amax:
+        k += 1
+    return 2.0 ** k
+
+
+def kv_append(values, scales, kv, cu_seqlens, table, past):
+    """New tokens' keys and values into the pages, in place.
+
+    values [num_pages, 2, 8, 64, 64]: what the codes stand for before the
+    scale (0: keys [head, token, dim], 1: values [head, dim, token]); scales
+    [num_pages, 2, 8]; kv [T, 2, 8, 64]: the new keys and values.  A touched
+    page's scale is kv_scale of its new finite values, not below the one it
+    has if it keeps tokens; kept tokens are rounded again where it rises;
+    infinities become NaN; a page begun here is zero behind its tokens."""
+    kv = _f64(kv)
+    for u in range(len(past)):
+        n, p, row = int(cu_seqlens[u + 1] - cu_seqlens[u]), int(past[u]), int(cu_seqlens[u])
+        done = 0
+        while done < n:
+            page, r = int(table[u][(p + done) // KV_PAGE]), (p + done) % KV_PAGE
+            m = min(KV_PAGE - r, n - done)
+            for side in range(2):
+                for h in range(8):
+                    x = kv[row + done:row + done + m, side, h]
+                    x = np.where(np.isfinite(x), x, np.nan)
+                    fin = np.abs(x[np.isfinite(x)])
+                    s = kv_scale(fin.max() if fin.size else 0.0)
+                    tile = values[page, side, h] if side == 0 else values[page, side, h].T  # [token, dim], a view
+                    if r == 0:
+                        tile[:] = 0.0
+                    else:
+                        old = scales[page, side, h]
+                        s = max(s, old)
+                        if s > old:
+                            tile[:r] = _e4m3_or_nan(tile[:r] * (old / s))
+                    tile[r:r + m] = _e4m3_or_nan(x / s)
+                    scales[page, side, h] = s
+            done += m
+    return values, scales
+
+
+def _e4m3_or_nan(x):
+    return np.where(np.isnan(x), np.nan, quantize_e4m3(np.nan_to_num(x, nan=0.0)))
+
+
+def paged_sequence(values, scales, pages, length):
+    """Keys and values [length, 8, 64] of a sequence with this page list."""
+    k = np.concatenate([(values[p, 0] * scales[p, 0][:, None, None]).transpose(1, 0, 2) for p in pages])[:length]
+    v = np.concatenate([(values[p, 1] * scales[p, 1][:, None, None]).transpose(2, 0, 1) for p in pages])[:length]
+    return k, v
+
+
+def attention_paged(q, values, scales, cu_seqlens, table, past, window=0, sinks=0, details=False):
+    """softmax(q K^T / 8) V of the new tokens over their sequence's pages: the
+    query at position i sees j <= i and, with window > 0, i - j < window or
+    j < sinks.  q [T, 8, 64] -> [T, 8, 64]; with details also sum_j p_j |v_j|
+    [T, 8, 64], max_j sum_d |q_d k_jd| / 8 [T, 8] and the visible keys' number [T]."""
+    q = _f64(q)
+    out, mag = np.zeros_like(q), np.zeros_like(q)
+    smax, count = np.zeros(q.shape[:2]), np.zeros(len(q), dtype=np.int64)
+    for u in range(len(past)):
+        b, e, p = int(cu_seqlens[u]), int(cu_seqlens[u + 1]), int(past[u])
+        if e == b:
+            continue
+        length = p + e - b
+        pages = [int(x) if x >= 0 else 0 for x in table[u][:-(-length // KV_PAGE)]]
+        k, v = paged_sequence(values, scales, pages, length)
+        for t in range(b, e):
+            i = p + t - b
+            j = np.arange(i + 1)
+            vis = j if window <= 0 else j[(i - j < window) | (j < sinks)]
+            kk, vv = k[vis], v[vis]
+            s = np.einsum("hd,jhd->hj", q[t], kk) / 8.0
+            w = np.exp(s - s.max(axis=1, keepdims=True))
+            w /= w.sum(axis=1, keepdims=True)
+            out[t] = np.einsum("hj,jhd->hd", w, vv)
+            if details:
+                mag[t] = np.einsum("hj,jhd->hd", w, np.abs(vv))
+                smax[t] = (np.einsum("hd,jhd->hj", np.abs(q[t]), np.abs(kk)) / 8.0).max(axis=1)
+                count[t] = len(vis)
+    return (out, mag, smax, count) if details else out
+
+
+
+# --------------------------------------------------------------------------
 # Gate (cti2026 README, SMoE structure: softmax -> top-2 -> renormalise)
 # --------------------------------------------------------------------------
 def gate_probs(xn2, w_gate, b_gate):

@@ -38,6 +38,8 @@ static const char* kind_name(int kind) {
     case PTL_KERNEL_HEAD: return "head";
     case PTL_KERNEL_COPY: return "copy";
     case PTL_KERNEL_COMBINE: return "combine";
+    case PTL_KERNEL_KV_APPEND: return "kv_append";
+    case PTL_KERNEL_KV_COPY: return "kv_copy";
     default: return "ptl";
   }
 }
@@ -432,6 +434,9 @@ const char* ptl_status_string(ptl_status s) {
     case PTL_ERR_TIMEOUT: return "a bounded device-side wait ran out";
     case PTL_ERR_BAD_IDS: return "an embedding id outside its table, or bag offsets not within 0 .. num_ids and non-decreasing";
     case PTL_ERR_BAD_MASK: return "attention mask: target_group_size < 1, causal not 0/1, or a user's contextual + candidate counts outside 0 .. its length";
+    case PTL_ERR_BAD_PAGE: return "a page number outside the cache, or positions outside the page table";
+    case PTL_ERR_CACHE_FULL: return "not enough free pages";
+    case PTL_ERR_NO_MEMORY: return "host memory allocation failed";
     case PTL_ERR_UNSUPPORTED: return "unsupported device (needs sm_100)";
   }
   return "unknown status";
@@ -778,6 +783,109 @@ ptl_status ptl_linear_fp8(const uint8_t* xq, const float* sx, const uint8_t* wq,
   EndMark end_mark{st};
   mark(st, PTL_KERNEL_GEMM_QKV);
   PTL_TRY(launch_gemm_fp8(ma, mb, mo, sx, sw, bias, int(rows), out_features, in_features, err, st));
+  return PTL_OK;
+}
+
+// What ptl_kv_append, ptl_attention_paged and ptl_kv_copy_pages check alike.
+static ptl_status check_kv(const ptl_kv_pages* kv) {
+  if (!kv || !kv->codes || !kv->scales) return PTL_ERR_NULL;
+  if (kv->num_pages < 1) return PTL_ERR_SHAPE;
+  if (!a16(kv->codes) || !a4(kv->scales)) return PTL_ERR_ALIGN;
+  return PTL_OK;
+}
+static ptl_status check_small_ws(const void* workspace, size_t ws_bytes, size_t need) {
+  if (!workspace) return PTL_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PTL_ERR_ALIGN;
+  return ws_bytes < need ? PTL_ERR_WORKSPACE : PTL_OK;
+}
+
+ptl_status ptl_kv_append(const void* qkv, const int32_t* cu_seqlens, int32_t num_users, int64_t total_tokens,
+                         ptl_dtype dt, const ptl_kv_pages* kv, const int32_t* page_table, int32_t max_pages,
+                         const int32_t* past_lens, void* workspace, size_t ws_bytes, void* stream) {
+  ApiRange nvtx_range{"ptl_kv_append"};
+  if (dt != PTL_F32 && dt != PTL_BF16) return PTL_ERR_DTYPE;
+  if (total_tokens < 0 || total_tokens >= (int64_t(1) << 31) || num_users < 1 || max_pages < 1 ||
+      max_pages > KV_MAX_PAGES)
+    return PTL_ERR_SHAPE;
+  ptl_status s;
+  if ((s = check_small_ws(workspace, ws_bytes, 256)) != PTL_OK) return s;
+  if (total_tokens == 0) return PTL_OK;
+  if ((s = check_kv(kv)) != PTL_OK) return s;
+  if (!qkv || !cu_seqlens || !page_table || !past_lens) return PTL_ERR_NULL;
+  if (!a16(qkv) || !a4(cu_seqlens) || !a4(page_table) || !a4(past_lens)) return PTL_ERR_ALIGN;
+  if ((s = device_ok()) != PTL_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int32_t* err = static_cast<int32_t*>(workspace);
+  mark(st, PTL_KERNEL_CLEAR);
+  if (cudaMemsetAsync(err, 0, sizeof(int32_t), st) != cudaSuccess) return PTL_ERR_CUDA;
+  EndMark end_mark{st};
+  mark(st, PTL_KERNEL_KV_APPEND);
+  const KvAppendArgs a{qkv, cu_seqlens, page_table, past_lens, kv->codes, kv->scales, err,
+                       kv->num_pages, max_pages, num_users, int(total_tokens)};
+  PTL_TRY(launch_kv_append(a, dt, st));
+  return PTL_OK;
+}
+
+ptl_status ptl_kv_copy_pages(const ptl_kv_pages* kv, const int32_t* src, const int32_t* dst, int64_t count,
+                             void* workspace, size_t ws_bytes, void* stream) {
+  ApiRange nvtx_range{"ptl_kv_copy_pages"};
+  if (count < 0 || count >= (int64_t(1) << 31)) return PTL_ERR_SHAPE;
+  ptl_status s;
+  if ((s = check_small_ws(workspace, ws_bytes, 256)) != PTL_OK) return s;
+  if (count == 0) return PTL_OK;
+  if ((s = check_kv(kv)) != PTL_OK) return s;
+  if (!src || !dst) return PTL_ERR_NULL;
+  if (!a4(src) || !a4(dst)) return PTL_ERR_ALIGN;
+  if ((s = device_ok()) != PTL_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int32_t* err = static_cast<int32_t*>(workspace);
+  mark(st, PTL_KERNEL_CLEAR);
+  if (cudaMemsetAsync(err, 0, sizeof(int32_t), st) != cudaSuccess) return PTL_ERR_CUDA;
+  EndMark end_mark{st};
+  mark(st, PTL_KERNEL_KV_COPY);
+  PTL_TRY(launch_kv_copy(kv->codes, kv->scales, kv->num_pages, src, dst, count, err, st));
+  return PTL_OK;
+}
+
+// The paged attention's workspace: the error word, the split units' counters
+// (cleared together by each call), the split units' parts.
+static constexpr size_t kPagedCounters = 256;
+static constexpr size_t kPagedClear = kPagedCounters + sizeof(int32_t) * PAGED_MAX_CTAS * H;
+
+size_t ptl_attention_paged_workspace_size(int64_t max_tokens, int32_t max_users, ptl_dtype dt) {
+  if (max_tokens < 0 || max_tokens >= (int64_t(1) << 31) || max_users < 1 || (dt != PTL_F32 && dt != PTL_BF16)) return 0;
+  return align_up(kPagedClear, 256) + paged_partial_bytes();
+}
+
+ptl_status ptl_attention_paged(const void* qkv, void* attn, const int32_t* cu_seqlens, int32_t num_users,
+                               int64_t total_tokens, ptl_dtype dt, const ptl_kv_pages* kv, const int32_t* page_table,
+                               int32_t max_pages, const int32_t* past_lens, int32_t window, int32_t sinks,
+                               void* workspace, size_t ws_bytes, void* stream) {
+  ApiRange nvtx_range{"ptl_attention_paged"};
+  if (dt != PTL_F32 && dt != PTL_BF16) return PTL_ERR_DTYPE;
+  if (total_tokens < 0 || total_tokens >= (int64_t(1) << 31) || num_users < 1 || max_pages < 1 ||
+      max_pages > KV_MAX_PAGES)
+    return PTL_ERR_SHAPE;
+  if (sinks < 0) return PTL_ERR_BAD_MASK;
+  ptl_status s;
+  if ((s = check_small_ws(workspace, ws_bytes, ptl_attention_paged_workspace_size(total_tokens, num_users, dt))) != PTL_OK)
+    return s;
+  if (total_tokens == 0) return PTL_OK;
+  if ((s = check_kv(kv)) != PTL_OK) return s;
+  if (!qkv || !attn || !cu_seqlens || !page_table || !past_lens) return PTL_ERR_NULL;
+  if (!a16(qkv) || !a16(attn) || !a4(cu_seqlens) || !a4(page_table) || !a4(past_lens)) return PTL_ERR_ALIGN;
+  if ((s = device_ok()) != PTL_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  mark(st, PTL_KERNEL_CLEAR);
+  if (cudaMemsetAsync(ws, 0, kPagedClear, st) != cudaSuccess) return PTL_ERR_CUDA;
+  EndMark end_mark{st};
+  mark(st, PTL_KERNEL_ATTENTION);
+  const PagedArgs a{qkv, attn, cu_seqlens, page_table, past_lens, kv->codes, kv->scales,
+                    reinterpret_cast<int32_t*>(ws), reinterpret_cast<int32_t*>(ws + kPagedCounters),
+                    reinterpret_cast<float*>(ws + align_up(kPagedClear, 256)), kv->num_pages, max_pages, num_users,
+                    int(total_tokens), window, sinks};
+  PTL_TRY(launch_attn_paged(a, dt, st));
   return PTL_OK;
 }
 

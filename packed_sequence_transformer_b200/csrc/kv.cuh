@@ -1,0 +1,108 @@
+// kv.cuh -- the 8-bit paged key/value cache: page layout, the arguments of its
+// kernels, which pages and keys a query sees, and the e4m3 conversions.
+//
+// A page holds PTL_KV_PAGE = 64 consecutive tokens of one sequence, 64 KB of
+// e4m3 codes: [2][8 heads][64][64] bytes, first the keys as [token][dim], then
+// the values as [dim][token].  Keys and values both lie along the axis that
+// their product sums over (the dims of Q K^T, the tokens of P V), so one 4 KB
+// tile is one plain copy, and 16 consecutive bytes of a row are 16 consecutive
+// steps of the contraction: no transposition when the pages are read, which
+// happens for every token served; it is paid once, in the append.
+#pragma once
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace ptl {
+
+constexpr int KV_PAGE = PTL_KV_PAGE;        // tokens of a page
+constexpr int KV_TILE = KV_PAGE * DH;       // bytes of one side of one head of a page
+constexpr int KV_SIDE = H * KV_TILE;        // bytes of the keys (or the values) of a page
+constexpr int KV_PAGE_BYTES = 2 * KV_SIDE;  // 65536
+constexpr int KV_MIN_EXP = -100;            // smallest scale 2^-100
+constexpr int PAGED_MAX_CTAS = 2 * 148;     // bound on the paged attention's grid (its workspace holds two parts per block)
+constexpr int KV_MAX_PAGES = (1 << 25) - 1;  // pages of a sequence: positions stay below 2^31
+
+struct KvAppendArgs {
+  const void* qkv;
+  const int32_t *cu, *table, *past;
+  uint8_t* codes;
+  float* scales;
+  int32_t* err;
+  int num_pages, max_pages, U, T;
+};
+
+struct PagedArgs {
+  const void* qkv;
+  void* out;
+  const int32_t *cu, *table, *past;
+  const uint8_t* codes;
+  const float* scales;
+  int32_t* err;
+  int32_t* counters;  // [CTA][head] parts of a split unit done so far
+  float* partial;     // [2 CTA + which][head] unfinished sums of split units
+  int num_pages, max_pages, U, T, window, sinks;
+};
+
+// One user's place in a call, checked: n new tokens behind `past` kept ones.
+// Returns the ptl_status that the user's offsets or positions break, or 0.
+__device__ __forceinline__ int kv_check_user(const int32_t* cu, const int32_t* past, int u, int U, int T,
+                                             int max_pages, int& n, int& p) {
+  const int c0 = cu[u], c1 = cu[u + 1];
+  p = past[u];
+  n = c1 - c0;
+  if ((u == 0 && c0 != 0) || c0 < 0 || c1 < c0 || c1 > T || (u == U - 1 && c1 != T)) return PTL_ERR_BAD_OFFSETS;
+  if (p < 0 || int64_t(p) + n > int64_t(max_pages) * KV_PAGE) return PTL_ERR_BAD_PAGE;
+  return 0;
+}
+
+// The pages that queries at positions p0 .. p1 of a sequence read: `sinks`
+// pages from the first one on, then the pages `first` .. last.
+struct PageSpan {
+  int sinks, first, count;
+  __device__ __forceinline__ int page(int k) const { return k < sinks ? k : first + k - sinks; }
+};
+__device__ __forceinline__ PageSpan page_span(int p0, int p1, int window, int sinks) {
+  PageSpan s{0, 0, (p1 >> 6) + 1};
+  if (window > 0 && p0 >= window) {
+    s.first = (p0 - window + 1) >> 6;
+    const int sp = (sinks >> 6) + ((sinks & 63) != 0);
+    s.sinks = sp < s.first ? sp : s.first;
+    s.count = s.sinks + (p1 >> 6) - s.first + 1;
+  }
+  return s;
+}
+
+// Bit b: does the query at position `pos` see token 64 * page + b (base = 64 *
+// page)?  Tokens up to itself, and with a window only the last `window` of
+// them and the first `sinks` of the sequence.
+__device__ __forceinline__ uint64_t page_visible(int pos, int base, int window, int sinks) {
+  const int hi = pos - base;
+  if (hi < 0) return 0;
+  uint64_t m = hi >= 63 ? ~0ull : (2ull << hi) - 1;
+  if (window > 0) {
+    const int lo = hi - window + 1;
+    const uint64_t in = lo <= 0 ? ~0ull : lo >= 64 ? 0ull : ~0ull << lo;
+    const int s = sinks - base;
+    m &= in | (s <= 0 ? 0ull : s >= 64 ? ~0ull : (1ull << s) - 1);
+  }
+  return m;
+}
+// Does every query at positions p0 .. p1 see all 64 tokens from base on?
+__device__ __forceinline__ bool page_all_visible(int p0, int p1, int base, int window, int sinks) {
+  return base + 63 <= p0 && (window <= 0 || p1 - base < window || base + 63 < sinks);
+}
+
+// Two e4m3 codes to two halves (exact: e4m3 is a subset of fp16; 0x7F and
+// 0xFF become NaN).
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
+  return r;
+}
+// 0x80 in each byte that holds a NaN code
+__device__ __forceinline__ uint32_t e4m3_nan_bytes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+}  // namespace ptl

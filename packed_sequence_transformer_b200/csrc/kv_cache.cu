@@ -1,0 +1,287 @@
+// kv_cache.cu -- writing the 8-bit paged key/value cache: the append of new
+// tokens and the copy of pages.
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "kv.cuh"
+#include "launch.h"
+#include "sm100.cuh"
+
+namespace ptl {
+using namespace sm100;
+
+// ------------------------------------------------------------------ append
+// For the touched page of a user and one of its sides, with x the new tokens'
+// values and, in a page that keeps r > 0 earlier tokens, s_old its scale:
+//   s = max(s_old if r > 0, the smallest power of two with max |x| <= 448 s),
+//   code = e4m3(x / s), and where s > s_old, kept codes = e4m3(code s_old / s).
+// A power of two divides exactly, so raising a scale costs a kept code nothing
+// unless it falls into e4m3's subnormals; with any other scale each raise
+// would round every kept code once more.
+//
+// A block of 512 threads takes one (page, side) at a time: warp (head, half)
+// holds 32 tokens of one head in registers (one read of the input), the two
+// halves of a head meet in shared memory for the maximum, and the codes leave
+// from the registers.  Values are turned to [dim][token] on the way out: a
+// lane holds 4 consecutive tokens of 8 dims, so a 32-bit word of 4 tokens is
+// built in registers, and the words of a warp are exchanged through a
+// swizzled 2 KB tile (granule ^ dim / 8: the 8 lanes that store one word of 8
+// different rows hit 8 different 16-byte bank groups).
+// Every block works the list of pages out of the offsets by itself (a sum per
+// thread and a scan), which costs it a microsecond and saves a launch.
+constexpr int KVA_THREADS = 512;
+
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
+  uint32_t out = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t h = e4m3x2_to_half2((w >> (16 * i)) & 0xFFFFu);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    out |= uint32_t(cvt_e4m3x2(f.x * ratio, f.y * ratio)) << (16 * i);
+  }
+  return out;
+}
+// 0xFF in the bytes [lo, hi) of a word (both cut to 0 .. 4)
+__device__ __forceinline__ uint32_t byte_range(int lo, int hi) {
+  lo = lo < 0 ? 0 : lo > 4 ? 4 : lo;
+  hi = hi < 0 ? 0 : hi > 4 ? 4 : hi;
+  return hi <= lo ? 0u : uint32_t(((1ull << (8 * hi)) - 1) & ~((1ull << (8 * lo)) - 1));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 2 : 1) kv_append_kernel(const KvAppendArgs a) {
+  constexpr int VEC = 16 / sizeof(T);   // elements of a 16-byte load
+  constexpr int NLD = 8 / VEC;          // loads of a lane's 8 dims
+  __shared__ int64_t s_scan[KVA_THREADS / 32];
+  __shared__ uint32_t s_amax[H][2];
+  __shared__ int s_item[4];
+  __shared__ __align__(16) uint8_t s_turn[KVA_THREADS / 32][KV_TILE / 2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int head = warp >> 1, half = warp & 1;
+  const int c = lane & 7, j = lane >> 3;  // dims 8c .. 8c + 7, token group
+  pdl_wait();
+  pdl_trigger();
+
+  // this thread's users, their touched pages
+  const int per = (a.U + KVA_THREADS - 1) / KVA_THREADS;
+  const int u_lo = min(tid * per, a.U), u_hi = min(u_lo + per, a.U);
+  int64_t mine = 0;
+  int bad = 0;
+  for (int u = u_lo; u < u_hi; ++u) {
+    int n, p;
+    const int e = kv_check_user(a.cu, a.past, u, a.U, a.T, a.max_pages, n, p);
+    bad |= e == 0 ? 0 : e == PTL_ERR_BAD_OFFSETS ? 1 : 2;
+    if (e == 0 && n > 0) mine += ((p + n - 1) >> 6) - (p >> 6) + 1;
+  }
+  if (__syncthreads_or(bad)) {  // every block sees the same offsets: nothing is written
+    const int offsets = __syncthreads_or(bad & 1);
+    if (blockIdx.x == 0 && tid == 0) set_error(a.err, offsets ? PTL_ERR_BAD_OFFSETS : PTL_ERR_BAD_PAGE);
+    return;
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  int64_t base = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < KVA_THREADS / 32; ++w) {
+    if (w < warp) base += s_scan[w];
+    total += s_scan[w];
+  }
+
+  for (int64_t it = blockIdx.x; it < 2 * total; it += gridDim.x) {
+    const int64_t ord = it >> 1;
+    const int side = int(it & 1);
+    if (ord >= base && ord < base + mine) {  // one thread's users hold the page
+      int64_t left = ord - base;
+      for (int u = u_lo; u < u_hi; ++u) {
+        const int c0 = a.cu[u], n = a.cu[u + 1] - c0, p = a.past[u];
+        const int64_t cnt = n > 0 ? ((p + n - 1) >> 6) - (p >> 6) + 1 : 0;
+        if (left < cnt) {
+          const int pg = (p >> 6) + int(left);
+          const int r = left == 0 ? p & 63 : 0;                // tokens that the page keeps
+          const int t0 = left == 0 ? 0 : 64 * pg - p;          // first new token of the page
+          s_item[0] = a.table[int64_t(u) * a.max_pages + pg];
+          s_item[1] = r;
+          s_item[2] = min(64 - r, n - t0);
+          s_item[3] = c0 + t0;
+          break;
+        }
+        left -= cnt;
+      }
+    }
+    __syncthreads();
+    const int page = s_item[0], r = s_item[1], m = s_item[2], row0 = s_item[3];
+    const bool ok = page >= 0 && page < a.num_pages;
+    if (!ok && tid == 0) set_error(a.err, PTL_ERR_BAD_PAGE);
+
+    // 32 tokens (8 per lane: two groups of 4 consecutive ones) x 8 dims
+    uint4 raw[8 * NLD];
+    const T* in = static_cast<const T*>(a.qkv) + D * (1 + side) + head * DH + 8 * c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int t = 32 * half + 4 * (j + 4 * (i >> 2)) + (i & 3);
+      const bool has = ok && t >= r && t < r + m;
+#pragma unroll
+      for (int k = 0; k < NLD; ++k)
+        raw[i * NLD + k] = has ? __ldcs(reinterpret_cast<const uint4*>(in + int64_t(row0 + t - r) * QKV_N + k * VEC))
+                               : make_uint4(0, 0, 0, 0);
+    }
+    auto value = [&](int i, int e) -> float {  // dim 8c + e of the lane's token i
+      const T* x = reinterpret_cast<const T*>(&raw[i * NLD]);
+      return to_f32<T>(x[e]);
+    };
+    // largest finite magnitude; NaN and infinities count as NaN
+    uint32_t mx = 0;
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t b = __float_as_uint(value(i, e)) & 0x7FFFFFFFu;
+        odd |= b >= 0x7F800000u;
+        mx = max(mx, b >= 0x7F800000u ? 0u : b);
+      }
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    odd = __any_sync(0xffffffffu, odd);
+    if (lane == 0) s_amax[head][half] = mx;
+    float* sp = a.scales + (int64_t(ok ? page : 0) * 2 + side) * H + head;
+    const float s_old = r > 0 ? *sp : 0.f;
+    __syncthreads();
+    if (!ok) continue;  // (uniform) the next round's first barrier orders s_item
+    mx = max(s_amax[head][0], s_amax[head][1]);
+    // smallest k with max |x| <= 448 * 2^k = 1.75 * 2^(k + 8)
+    const int ke = max(int((mx + 0x1FFFFFu) >> 23) - 127 - 8, KV_MIN_EXP);
+    const float s = fmaxf(s_old, __uint_as_float(uint32_t(ke + 127) << 23));
+    const float inv = __fdiv_rn(1.0f, s), ratio = s_old * inv;
+    const bool grow = r > 0 && s > s_old;
+    if (half == 0 && lane == 0) *sp = s;
+    auto scaled = [&](int i, int e) -> float {
+      const float x = value(i, e);
+      if (odd && (__float_as_uint(x) & 0x7FFFFFFFu) >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
+      return x * inv;
+    };
+    uint8_t* tile = a.codes + int64_t(page) * KV_PAGE_BYTES + side * KV_SIDE + head * KV_TILE;
+    if (side == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int t = 32 * half + 4 * (j + 4 * (i >> 2)) + (i & 3);
+        uint2* dst = reinterpret_cast<uint2*>(tile + t * DH + 8 * c);
+        if (t >= r && (t < r + m || r == 0)) {  // a page begun by this call is written whole, zeros behind the tokens
+          uint2 w;
+          w.x = uint32_t(cvt_e4m3x2(scaled(i, 0), scaled(i, 1))) | uint32_t(cvt_e4m3x2(scaled(i, 2), scaled(i, 3))) << 16;
+          w.y = uint32_t(cvt_e4m3x2(scaled(i, 4), scaled(i, 5))) | uint32_t(cvt_e4m3x2(scaled(i, 6), scaled(i, 7))) << 16;
+          *dst = w;
+        } else if (t < r && grow) {
+          const uint2 w = *dst;
+          *dst = make_uint2(rescale4(w.x, ratio), rescale4(w.y, ratio));
+        }
+      }
+    } else {
+      uint8_t* turn = s_turn[warp];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int d = 8 * c + e;
+          const uint32_t w = uint32_t(cvt_e4m3x2(scaled(4 * q, e), scaled(4 * q + 1, e))) |
+                             uint32_t(cvt_e4m3x2(scaled(4 * q + 2, e), scaled(4 * q + 3, e))) << 16;
+          *reinterpret_cast<uint32_t*>(turn + 16 * ((2 * d + q) ^ c) + 4 * j) = w;
+        }
+      __syncwarp();
+      const int t_lo = 32 * half;
+      const bool touched = (r < t_lo + 32 && r + m > t_lo) || (grow && t_lo < r);
+      if (r == 0 || touched) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int d = lane + 32 * k;
+          uint4 w[2];
+          uint4* dst = reinterpret_cast<uint4*>(tile + d * KV_PAGE + t_lo);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) w[q] = *reinterpret_cast<const uint4*>(turn + 16 * ((2 * d + q) ^ (d >> 3)));
+          if (r > 0) {  // the row's other bytes stay (or are rescaled)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint4 o = dst[q];
+              uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
+              uint32_t* nw = reinterpret_cast<uint32_t*>(&w[q]);
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                const int t = t_lo + 16 * q + 4 * b;
+                const uint32_t isnew = byte_range(r - t, r + m - t);
+                uint32_t keep = ow[b];
+                if (grow) {
+                  const uint32_t kept = byte_range(0, r - t);
+                  keep = (rescale4(keep, ratio) & kept) | (keep & ~kept);
+                }
+                nw[b] = (nw[b] & isnew) | (keep & ~isnew);
+              }
+            }
+          }
+          dst[0] = w[0];
+          dst[1] = w[1];
+        }
+      }
+      __syncwarp();  // the tile is read before the next page's words are stored
+    }
+  }
+}
+
+int launch_kv_append(const KvAppendArgs& a, ptl_dtype dt, cudaStream_t st) {
+  // at most T / 64 + 2 pages per user with tokens are touched, two sides each
+  const int64_t users = a.U < a.T ? a.U : a.T;
+  const int64_t items = 2 * (a.T / KV_PAGE + 2 * users);
+  const int64_t most = int64_t(num_sms()) * (dt == PTL_BF16 ? 2 : 1);
+  const dim3 grid(unsigned(items < most ? items : most));
+  const int r = dt == PTL_BF16 ? launch_k(kv_append_kernel<__nv_bfloat16>, grid, dim3(KVA_THREADS), 0, st, a)
+                               : launch_k(kv_append_kernel<float>, grid, dim3(KVA_THREADS), 0, st, a);
+  return r != 0 ? -1 : cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+// -------------------------------------------------------------- page copy
+// Page dst[i] becomes a copy of page src[i], codes and scales.  A block moves a
+// quarter of a page (16 KB) at a time, four 16-byte loads of each thread in
+// flight before the first store.
+constexpr int KVC_THREADS = 256;
+constexpr int KVC_PARTS = KV_PAGE_BYTES / (KVC_THREADS * 64);
+
+__global__ void __launch_bounds__(KVC_THREADS) kv_copy_kernel(uint8_t* codes, float* scales, int num_pages,
+                                                              const int32_t* __restrict__ src,
+                                                              const int32_t* __restrict__ dst, int64_t n,
+                                                              int32_t* err) {
+  pdl_wait();
+  pdl_trigger();
+  for (int64_t it = blockIdx.x; it < n * KVC_PARTS; it += gridDim.x) {
+    const int64_t i = it / KVC_PARTS;
+    const int part = int(it % KVC_PARTS);
+    const int s = src[i], d = dst[i];
+    if (s < 0 || s >= num_pages || d < 0 || d >= num_pages) {
+      if (threadIdx.x == 0) set_error(err, PTL_ERR_BAD_PAGE);
+      continue;
+    }
+    const uint4* from = reinterpret_cast<const uint4*>(codes + int64_t(s) * KV_PAGE_BYTES) + part * KVC_THREADS * 4;
+    uint4* to = reinterpret_cast<uint4*>(codes + int64_t(d) * KV_PAGE_BYTES) + part * KVC_THREADS * 4;
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = from[k * KVC_THREADS + threadIdx.x];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) to[k * KVC_THREADS + threadIdx.x] = v[k];
+    if (part == 0 && threadIdx.x < 2 * H) scales[int64_t(d) * 2 * H + threadIdx.x] = scales[int64_t(s) * 2 * H + threadIdx.x];
+  }
+}
+
+int launch_kv_copy(uint8_t* codes, float* scales, int num_pages, const int32_t* src, const int32_t* dst, int64_t n,
+                   int32_t* err, cudaStream_t st) {
+  const int64_t items = n * KVC_PARTS, most = int64_t(num_sms()) * 8;
+  const int r = launch_k(kv_copy_kernel, dim3(unsigned(items < most ? items : most)), dim3(KVC_THREADS), 0, st, codes,
+                         scales, num_pages, src, dst, n, err);
+  return r != 0 ? -1 : cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace ptl

@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "kv.cuh"
 
 namespace ptl {
 
@@ -174,6 +175,14 @@ int launch_gemm_moe2(const CUtensorMap& hbuf, const CUtensorMap& w2, const CUten
 // codes with per-row scales, 256 x 256 pair tiles (K a multiple of 128, N of 256)
 int launch_gemm_fp8(const CUtensorMap& xq, const CUtensorMap& wq, const CUtensorMap& out_map, const float* sx,
                     const float* sw, const float* bias, int M, int N, int Kd, int32_t* err, cudaStream_t st);
+
+// kv_cache.cu: new tokens into the paged cache; page dst[i] = page src[i]
+int launch_kv_append(const KvAppendArgs& a, ptl_dtype dt, cudaStream_t st);
+int launch_kv_copy(uint8_t* codes, float* scales, int num_pages, const int32_t* src, const int32_t* dst, int64_t n,
+                   int32_t* err, cudaStream_t st);
+// attn_paged.cu: attention over the paged cache (the counters must be zero)
+size_t paged_partial_bytes();
+int launch_attn_paged(const PagedArgs& a, ptl_dtype dt, cudaStream_t st);
 
 // attn_tc.cu (bf16, tcgen05)
 // mask (nullable): the HSTU-style variant, over a work list built with the

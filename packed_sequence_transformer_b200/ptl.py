@@ -9,6 +9,7 @@ raises; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Dict, Iterable, List, Optional
@@ -23,6 +24,7 @@ STATUS = {
     0: "PTL_OK", 1: "PTL_ERR_NULL", 2: "PTL_ERR_ALIGN", 3: "PTL_ERR_SHAPE",
     4: "PTL_ERR_BAD_OFFSETS", 5: "PTL_ERR_WORKSPACE", 6: "PTL_ERR_DTYPE", 7: "PTL_ERR_CUDA",
     8: "PTL_ERR_TIMEOUT", 9: "PTL_ERR_UNSUPPORTED", 10: "PTL_ERR_BAD_MASK", 11: "PTL_ERR_BAD_IDS",
+    12: "PTL_ERR_BAD_PAGE", 13: "PTL_ERR_CACHE_FULL", 14: "PTL_ERR_NO_MEMORY",
 }
 STATUS_CODE = {v: k for k, v in STATUS.items()}
 
@@ -65,6 +67,10 @@ class RepWeightsStruct(ctypes.Structure):
                 ("b", ctypes.c_void_p)]
 
 
+class KvPagesStruct(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("num_pages", ctypes.c_int32)]
+
+
 class Trace(ctypes.Structure):
     _fields_ = [("events", ctypes.POINTER(ctypes.c_void_p)), ("kinds", ctypes.POINTER(ctypes.c_int32)),
                 ("capacity", ctypes.c_int32), ("count", ctypes.c_int32)]
@@ -72,9 +78,11 @@ class Trace(ctypes.Structure):
 
 KERNEL_KINDS = {0: "clear", 1: "worklist", 2: "layernorm", 3: "gemm_qkv", 4: "attention",
                 5: "gemm_out", 6: "gate", 7: "route", 8: "gemm_expert1", 9: "gemm_expert2",
-                10: "head", 11: "copy", 12: "combine", 99: "end"}
+                10: "head", 11: "copy", 12: "combine", 13: "kv_append", 14: "kv_copy",
+                99: "end"}
 
 _lib = None
+_I32P = ctypes.POINTER(ctypes.c_int32)
 _SIGS = {
     "ptl_version": ([], ctypes.c_int32),
     "ptl_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -140,6 +148,27 @@ _SIGS = {
     "ptl_linear_fp8": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                         ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                         ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int),
+    "ptl_kv_append": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int,
+                       ctypes.POINTER(KvPagesStruct), ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                       ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int),
+    "ptl_attention_paged_workspace_size": ([ctypes.c_int64, ctypes.c_int32, ctypes.c_int], ctypes.c_size_t),
+    "ptl_attention_paged": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
+                             ctypes.c_int, ctypes.POINTER(KvPagesStruct), ctypes.c_void_p, ctypes.c_int32,
+                             ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t,
+                             ctypes.c_void_p], ctypes.c_int),
+    "ptl_kv_copy_pages": ([ctypes.POINTER(KvPagesStruct), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                           ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int),
+    "ptl_kv_pool_create": ([ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_void_p)], ctypes.c_int),
+    "ptl_kv_pool_destroy": ([ctypes.c_void_p], None),
+    "ptl_kv_pool_reserve": ([ctypes.c_void_p, _I32P, _I32P, ctypes.c_int32], ctypes.c_int),
+    "ptl_kv_pool_fork": ([ctypes.c_void_p, _I32P, _I32P, ctypes.c_int32, _I32P, _I32P, _I32P], ctypes.c_int),
+    "ptl_kv_pool_release": ([ctypes.c_void_p, _I32P, ctypes.c_int32], ctypes.c_int),
+    "ptl_kv_pool_trim": ([ctypes.c_void_p, _I32P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _I32P],
+                         ctypes.c_int),
+    "ptl_kv_pool_compact": ([ctypes.c_void_p, ctypes.c_int32, _I32P, _I32P, _I32P], ctypes.c_int),
+    "ptl_kv_pool_table": ([ctypes.c_void_p, _I32P, ctypes.c_int32, ctypes.c_int32, _I32P], ctypes.c_int),
+    "ptl_kv_pool_length": ([ctypes.c_void_p, ctypes.c_int32], ctypes.c_int32),
+    "ptl_kv_pool_free_pages": ([ctypes.c_void_p], ctypes.c_int32),
     "ptl_partition_users": ([ctypes.POINTER(ctypes.c_int32), ctypes.c_int32, ctypes.c_int32,
                              ctypes.POINTER(ctypes.c_int32)], ctypes.c_int),
 }
@@ -192,6 +221,12 @@ def _stream(stream) -> ctypes.c_void_p:
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
+
+
+def _on(t: torch.Tensor):
+    """The device of a call's tensors, as the current one (CPU tensors: as it is,
+    the library then refuses or returns without work)."""
+    return torch.cuda.device(t.device) if t.is_cuda else contextlib.nullcontext()
 
 
 def torch_dtype(dt) -> torch.dtype:
@@ -402,6 +437,182 @@ def linear_fp8(xq, sx, wq, sw, bias, out, workspace, stream=None):
     _check(lib().ptl_linear_fp8(_ptr(xq), _ptr(sx), _ptr(wq), _ptr(sw), _ptr(bias), _ptr(out), M, K, N,
                                 _ptr(workspace), workspace.numel(), _stream(stream)), "ptl_linear_fp8")
     return out
+
+
+# ------------------------------------------------- the 8-bit paged key/value cache
+KV_PAGE = 64
+
+
+class KvPages:
+    """One layer's pages (``ptl_kv_pages``): codes uint8 [num_pages, 2, 8, 64, 64]
+    and scales float32 [num_pages, 2, 8], device tensors that the caller keeps."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        n = codes.shape[0]
+        if codes.dtype != torch.uint8 or tuple(codes.shape) != (n, 2, 8, KV_PAGE, 64):
+            raise ValueError("codes must be uint8 [num_pages, 2, 8, 64, 64]")
+        if scales.dtype != torch.float32 or tuple(scales.shape) != (n, 2, 8):
+            raise ValueError("scales must be float32 [num_pages, 2, 8]")
+        if scales.device != codes.device:
+            raise ValueError("codes and scales must be on one device")
+        self.codes, self.scales = codes, scales
+        self._struct = KvPagesStruct(_ptr(codes), _ptr(scales), n)
+
+
+def alloc_kv_pages(num_pages: int, device="cuda") -> KvPages:
+    """Pages of zeros for one layer (65,600 bytes each)."""
+    return KvPages(torch.zeros(num_pages, 2, 8, KV_PAGE, 64, dtype=torch.uint8, device=device),
+                   torch.ones(num_pages, 2, 8, dtype=torch.float32, device=device))
+
+
+def _check_paged(qkv, cu_seqlens, kv: KvPages, page_table, past_lens, workspace, attn=None):
+    """Shapes, types and devices of a call on the paged cache; its users and table width."""
+    users = past_lens.numel()
+    if qkv.dim() != 2 or qkv.shape[1] != 1536:
+        raise ValueError("qkv must be [T, 1536]")
+    if attn is not None and (tuple(attn.shape) != (qkv.shape[0], 512) or attn.dtype != qkv.dtype):
+        raise ValueError("attn must be [T, 512] of qkv's dtype")
+    if cu_seqlens.numel() != users + 1 or page_table.dim() != 2 or page_table.shape[0] != users:
+        raise ValueError("cu_seqlens [U + 1], page_table [U, max_pages] and past_lens [U] do not agree")
+    for t in (cu_seqlens, page_table, past_lens):
+        if t.dtype != torch.int32:
+            raise ValueError("cu_seqlens, page_table and past_lens must be int32")
+    for t in (cu_seqlens, kv.codes, page_table, past_lens, workspace) + (() if attn is None else (attn,)):
+        if t.device != qkv.device:
+            raise ValueError("all tensors of a call must be on one device")
+    return users, page_table.shape[1]
+
+
+def kv_append(qkv, cu_seqlens, kv: KvPages, page_table, past_lens, workspace, stream=None):
+    """ptl_kv_append: the keys and values of qkv [T, 1536] into the pages, token
+    i of user u at position past_lens[u] + i.  workspace: >= 256 bytes."""
+    U, max_pages = _check_paged(qkv, cu_seqlens, kv, page_table, past_lens, workspace)
+    with _on(qkv):
+        _check(lib().ptl_kv_append(_ptr(qkv), _ptr(cu_seqlens), U, qkv.shape[0], _dt(qkv.dtype),
+                                   ctypes.byref(kv._struct), _ptr(page_table), max_pages, _ptr(past_lens),
+                                   _ptr(workspace), workspace.numel(), _stream(stream)), "ptl_kv_append")
+    return kv
+
+
+def attention_paged_workspace(max_tokens: int, max_users: int, dtype, device="cuda") -> torch.Tensor:
+    n = int(lib().ptl_attention_paged_workspace_size(int(max_tokens), int(max_users), _dt(dtype)))
+    if n == 0:
+        raise ValueError("invalid workspace request")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def attention_paged(qkv, attn, cu_seqlens, kv: KvPages, page_table, past_lens, workspace, window=0, sinks=0,
+                    stream=None):
+    """ptl_attention_paged: the new tokens' attention over the pages (which
+    hold the new tokens too), causal, with window > 0 only the last `window`
+    keys and the sequence's first `sinks`, into attn [T, 512]."""
+    U, max_pages = _check_paged(qkv, cu_seqlens, kv, page_table, past_lens, workspace, attn)
+    with _on(qkv):
+        _check(lib().ptl_attention_paged(_ptr(qkv), _ptr(attn), _ptr(cu_seqlens), U, qkv.shape[0], _dt(qkv.dtype),
+                                         ctypes.byref(kv._struct), _ptr(page_table), max_pages, _ptr(past_lens),
+                                         int(window), int(sinks), _ptr(workspace), workspace.numel(),
+                                         _stream(stream)), "ptl_attention_paged")
+    return attn
+
+
+def kv_copy_pages(kv: KvPages, src, dst, workspace, stream=None):
+    """ptl_kv_copy_pages: page dst[i] = page src[i] (device int32 lists, as
+    ``KvPool.fork`` and ``KvPool.compact`` give them).  workspace: >= 256 bytes."""
+    if src.dtype != torch.int32 or dst.dtype != torch.int32 or src.shape != dst.shape or src.dim() != 1:
+        raise ValueError("src and dst must be int32 lists of one length")
+    if any(t.device != kv.codes.device for t in (src, dst, workspace)):
+        raise ValueError("all tensors of a call must be on one device")
+    with _on(kv.codes):
+        _check(lib().ptl_kv_copy_pages(ctypes.byref(kv._struct), _ptr(src), _ptr(dst), src.numel(), _ptr(workspace),
+                                       workspace.numel(), _stream(stream)), "ptl_kv_copy_pages")
+    return kv
+
+
+class KvPool:
+    """Whose pages are whose (``ptl_kv_pool_*``): host bookkeeping of num_seqs
+    sequences over num_pages pages.  One pool serves all layers; each layer has
+    its own ``KvPages``.  Lists come back as int32 CPU tensors."""
+
+    def __init__(self, num_pages: int, num_seqs: int):
+        p = ctypes.c_void_p()
+        _check(lib().ptl_kv_pool_create(int(num_pages), int(num_seqs), ctypes.byref(p)), "ptl_kv_pool_create")
+        self._p = p
+        self.num_pages, self.num_seqs = num_pages, num_seqs
+
+    @staticmethod
+    def _list(values):
+        t = torch.as_tensor(values, dtype=torch.int32, device="cpu").reshape(-1).contiguous()
+        return t, ctypes.cast(t.data_ptr(), _I32P), t.numel()
+
+    def reserve(self, seqs, new_lens) -> None:
+        """Room for sequence seqs[i] to hold new_lens[i] tokens in all."""
+        (s, sp, n), (l, lp, m) = self._list(seqs), self._list(new_lens)
+        if n != m:
+            raise ValueError("one length per sequence")
+        _check(lib().ptl_kv_pool_reserve(self._p, sp, lp, n), "ptl_kv_pool_reserve")
+
+    def fork(self, src, dst):
+        """Empty sequences dst become copies of src; the (source, destination)
+        pages that ``kv_copy_pages`` has to copy in every layer."""
+        (s, sp, n), (d, dp, m) = self._list(src), self._list(dst)
+        if n != m:
+            raise ValueError("one destination per source")
+        a, b = torch.empty(n, dtype=torch.int32), torch.empty(n, dtype=torch.int32)
+        k = ctypes.c_int32()
+        _check(lib().ptl_kv_pool_fork(self._p, sp, dp, n, ctypes.cast(a.data_ptr(), _I32P),
+                                      ctypes.cast(b.data_ptr(), _I32P), ctypes.byref(k)), "ptl_kv_pool_fork")
+        return a[:k.value], b[:k.value]
+
+    def release(self, seqs) -> None:
+        s, sp, n = self._list(seqs)
+        _check(lib().ptl_kv_pool_release(self._p, sp, n), "ptl_kv_pool_release")
+
+    def trim(self, seqs, window: int, sinks: int = 0) -> int:
+        """Gives up the pages that no later token can see; how many became free."""
+        s, sp, n = self._list(seqs)
+        k = ctypes.c_int32()
+        _check(lib().ptl_kv_pool_trim(self._p, sp, n, int(window), int(sinks), ctypes.byref(k)), "ptl_kv_pool_trim")
+        return k.value
+
+    def compact(self):
+        """Moves pages down so that the used ones come first; the (source,
+        destination) pages that ``kv_copy_pages`` has to copy in every layer."""
+        k = self.num_pages - self.free_pages
+        a, b = torch.empty(k, dtype=torch.int32), torch.empty(k, dtype=torch.int32)
+        moved = ctypes.c_int32()
+        _check(lib().ptl_kv_pool_compact(self._p, k, ctypes.cast(a.data_ptr(), _I32P),
+                                         ctypes.cast(b.data_ptr(), _I32P), ctypes.byref(moved)),
+               "ptl_kv_pool_compact")
+        return a[:moved.value], b[:moved.value]
+
+    def table(self, seqs, max_pages: Optional[int] = None) -> torch.Tensor:
+        """The page table [len(seqs), max_pages] of these sequences (by default
+        as wide as the longest list needs)."""
+        s, sp, n = self._list(seqs)
+        if max_pages is None:
+            max_pages = max([1] + [-(-self.length(q) // KV_PAGE) for q in s.tolist()])
+        t = torch.empty(n, max_pages, dtype=torch.int32)
+        _check(lib().ptl_kv_pool_table(self._p, sp, n, int(max_pages), ctypes.cast(t.data_ptr(), _I32P)),
+               "ptl_kv_pool_table")
+        return t
+
+    def length(self, seq: int) -> int:
+        return int(lib().ptl_kv_pool_length(self._p, int(seq)))
+
+    @property
+    def free_pages(self) -> int:
+        return int(lib().ptl_kv_pool_free_pages(self._p))
+
+    def close(self) -> None:
+        if getattr(self, "_p", None):
+            lib().ptl_kv_pool_destroy(self._p)
+            self._p = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 def partition_users(cu_seqlens, num_parts: int):

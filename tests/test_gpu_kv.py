@@ -1,0 +1,435 @@
+"""The 8-bit paged key/value cache on the GPU: the append's codes and scales
+bit for bit against the oracle, the attention over the pages elementwise
+within the bound that its roundings allow, the page copy, and all of them
+together as a served layer uses them."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import ptl_oracle as O
+from packed_sequence_transformer_b200 import ptl
+from packed_sequence_transformer_b200 import synthetic as S
+from tests.gpu_util import dev, host, tdt
+from tests.kv_util import Call, make_pages, value_of_codes
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ptl.lib()
+
+
+def _expect_append(c):
+    return O.kv_append(value_of_codes(torch.from_numpy(c.codes)), c.scales.astype(np.float64),
+                       c.qkv[:, 512:].reshape(c.T, 2, 8, 64), c.cu, c.table, c.past)
+
+
+def _check_append(c, want):
+    ws = c.append()
+    torch.cuda.synchronize()
+    assert ptl.last_device_error(ws) == 0
+    np.testing.assert_array_equal(host(c.kv.scales), want[1])
+    np.testing.assert_array_equal(value_of_codes(c.kv.codes), want[0])
+
+
+# ---------------------------------------------------------------- append
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("new,past", [
+    ([1], [0]), ([1], [63]), ([1], [64]), ([2], [63]), ([64], [0]), ([65], [0]), ([130], [31]),
+    ([0, 1, 0, 5, 70, 0], [3, 9, 0, 62, 1, 0]),
+    ([1] * 40, list(range(25, 65))),
+    ([33, 31, 32, 0, 200], [32, 33, 31, 7, 0]),
+])
+def test_append_codes_and_scales(dt, new, past):
+    c = Call(len(new) * 100 + new[-1], new, past, dt)
+    _check_append(c, _expect_append(c))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_append_raises_scales_step_by_step(dt):
+    """One token at a time, each larger than all before it: every step raises
+    the scale and rounds the kept codes again."""
+    steps = 70
+    c = Call(3, [1, 1], [0, 0], dt, num_pages=5)
+    c.table = np.array([[4, 1], [0, 2]], np.int32)
+    vals, sc = value_of_codes(torch.from_numpy(c.codes)), c.scales.astype(np.float64)
+    c.upload()
+    base = c.rng.standard_normal((steps, 2, 1536)).astype(np.float32)
+    for k in range(steps):
+        c.qkv_d = dev(base[k] * np.float32(1.3 ** k), tdt(dt))
+        c.qkv, c.past = host(c.qkv_d), [k, k]
+        c.past_d = dev(np.array(c.past), torch.int32)
+        ws = c.append()
+        O.kv_append(vals, sc, c.qkv[:, 512:].reshape(2, 2, 8, 64), c.cu, c.table, c.past)
+    torch.cuda.synchronize()
+    assert ptl.last_device_error(ws) == 0
+    np.testing.assert_array_equal(host(c.kv.scales), sc)
+    np.testing.assert_array_equal(value_of_codes(c.kv.codes), vals)
+
+
+def test_append_extremes():
+    """Zeros, the smallest and largest numbers, exact borders of the scale, and
+    what is no number."""
+    c = Call(5, [8, 4], [0, 60], "fp32")
+    x = c.qkv.copy().astype(np.float32).reshape(12, 3, 8, 64)
+    x[:8, 1:, 0] = 0.0
+    x[:8, 1:, 1] = 1e-45
+    x[:8, 1:, 2] = 448.0 * 2.0 ** 5
+    x[:8, 1:, 3] = np.nextafter(np.float32(448.0 * 2.0 ** 5), np.float32(np.inf))
+    x[:8, 1:, 4] = np.finfo(np.float32).max
+    x[3, 1, 5, 7], x[4, 2, 5, 9], x[5, 2, 5, 63] = np.nan, np.inf, -np.inf
+    x[:8, 1:, 6] = np.nan
+    x[9, 1, 7, 0] = 2.0 ** 100
+    c.qkv_d = dev(x.reshape(12, 1536), torch.float32)
+    c.upload()
+    want = _expect_append(c)
+    _check_append(c, want)
+    assert np.isnan(want[0]).any()
+
+
+def test_append_again_after_taking_tokens_back():
+    c = Call(6, [5, 9], [62, 3])
+    c.append()
+    torch.cuda.synchronize()
+    c.codes, c.scales = c.kv.codes.cpu().numpy(), c.kv.scales.cpu().numpy()
+    c.qkv_d = dev(c.rng.standard_normal((14, 1536)).astype(np.float32), torch.bfloat16)
+    c.upload()
+    _check_append(c, _expect_append(c))
+
+
+def test_append_reports_and_leaves_the_rest():
+    # a page number out of range: that page is skipped, the other is written
+    c = Call(7, [10, 10], [0, 0])
+    good = c.table.copy()
+    for bad in (-1, c.num_pages, 2 ** 31 - 1, -2 ** 31):
+        c.table = good.copy()
+        c.table[0, 0] = bad
+        c.upload()
+        ws = c.append()
+        torch.cuda.synchronize()
+        assert ptl.last_device_error(ws) == ptl.STATUS_CODE["PTL_ERR_BAD_PAGE"]
+        got = c.kv.codes.cpu().numpy()
+        changed = [p for p in range(c.num_pages) if not np.array_equal(got[p], c.codes[p])]
+        assert changed == [good[1, 0]]
+    # positions or offsets that do not fit: nothing is written
+    for cu, past, err in [([0, 10, 20], [60, 0], "PTL_ERR_BAD_PAGE"), ([0, 10, 20], [-1, 0], "PTL_ERR_BAD_PAGE"),
+                          ([0, 10, 20], [2 ** 31 - 1, 0], "PTL_ERR_BAD_PAGE"),
+                          ([0, 10, 19], [0, 0], "PTL_ERR_BAD_OFFSETS"), ([1, 10, 20], [0, 0], "PTL_ERR_BAD_OFFSETS"),
+                          ([0, 21, 20], [0, 0], "PTL_ERR_BAD_OFFSETS"), ([0, -5, 20], [0, 0], "PTL_ERR_BAD_OFFSETS")]:
+        c.table = good
+        c.upload()
+        c.cu_d, c.past_d = dev(np.array(cu), torch.int32), dev(np.array(past), torch.int32)
+        ws = c.append()
+        out, ws2 = c.attend()
+        torch.cuda.synchronize()
+        assert ptl.last_device_error(ws) == ptl.STATUS_CODE[err]
+        assert ptl.last_device_error(ws2) == ptl.STATUS_CODE[err]
+        assert np.array_equal(c.kv.codes.cpu().numpy(), c.codes)
+        assert np.array_equal(c.kv.scales.cpu().numpy(), c.scales)
+        assert torch.isnan(out).all()
+
+
+# ------------------------------------------------------------- attention
+SHAPES = [
+    ([1], [0]), ([1], [1]), ([1], [62]), ([1], [63]), ([1], [64]), ([1], [500]),
+    ([3], [0]), ([8], [120]), ([9], [120]), ([17], [55]), ([70], [0]), ([200], [0]), ([129], [131]),
+    ([0, 1, 0, 2, 90, 0], [77, 0, 0, 130, 10, 5]),
+    ([1] * 33, [7 * i for i in range(33)]),
+]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("new,past", SHAPES)
+def test_attention_against_the_oracle(dt, new, past):
+    Call(new[0] * 7 + past[0] + len(new), new, past, dt).check()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 4), (63, 0), (64, 64), (65, 65), (100, 3), (128, 200),
+                                          (5, 2 ** 31 - 1), (2 ** 31 - 1, 0), (300, 1000), (0, 7), (-4, 0)])
+def test_attention_window_and_sinks(dt, window, sinks):
+    Call(window % 1000 + sinks % 1000, [1, 5, 200, 0, 1, 130], [700, 64, 90, 9, 0, 319], dt).check(window, sinks)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_attention_many_parts(dt):
+    """One history over more blocks than the grid has, and users whose pages end
+    inside a block's range."""
+    Call(11, [1], [20000], dt).check()
+    Call(12, [2, 1, 9, 1], [9000, 10, 4000, 12345], dt).check()
+    Call(13, [1, 1], [15000, 15000], dt).check(window=9000, sinks=70)
+
+
+def test_attention_many_users():
+    """More users than a block has threads."""
+    rng = np.random.default_rng(14)
+    Call(14, rng.integers(0, 3, 700).tolist(), rng.integers(0, 150, 700).tolist()).check()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_attention_magnitudes(dt):
+    """Rows of q from tiny to huge, scales far apart from page to page."""
+    c = Call(15, [16, 6], [200, 300], dt)
+    x = host(c.qkv_d).astype(np.float32)
+    x[:, :512] *= (10.0 ** np.linspace(-30, 1, 22))[:, None].astype(np.float32)
+    x[3, :512] = 0.0
+    c.qkv_d = dev(x, tdt(dt))
+    c.scales[:, 1] *= (2.0 ** c.rng.integers(-30, 20, (c.num_pages, 8))).astype(np.float32)
+    c.upload()
+    c.check()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("new,past", [([3, 1], [100, 700]), ([150, 40], [100, 700])])
+def test_masked_places_have_no_effect(dt, new, past):
+    """NaN codes behind the last token, before the window, and in front of
+    later queries; visible ones reach the queries that see them."""
+    c = Call(16, new, past, dt)
+    nan = np.uint8(0x7F)
+    # behind the end
+    for u in range(2):
+        end = new[u] + past[u]
+        page = c.table[u, (end - 1) // 64]
+        c.codes[page, 0, :, end % 64 or 64:], c.codes[page, 1, :, :, end % 64 or 64:] = nan, np.uint8(0xFF)
+    c.upload()
+    c.check()
+    # user 1: a key and a value that some queries see through the window and others do not
+    at = past[1] - 20
+    page = c.table[1, at // 64]
+    c.codes[page, 1, 2, 5, at % 64] = nan
+    c.codes[page, 1, 3, 40, at % 64] = np.uint8(0xFF)
+    c.codes[page, 0, 6, at % 64, 11] = nan
+    c.upload()
+    c.check(window=30, sinks=1)
+    c.check(window=21, sinks=1)
+    c.check(window=20, sinks=1)
+    c.check()
+    # in a row of the call itself: later queries see it, earlier ones do not
+    at = past[0] + new[0] - 2
+    page = c.table[0, at // 64]
+    c.codes[page, 1, 0, 0, at % 64] = nan
+    c.upload()
+    out = c.check()
+    assert torch.isnan(out[new[0] - 2:new[0], 0]).all() and torch.isfinite(out[:new[0] - 2, 0]).all()
+
+
+def test_infinite_queries_stay_in_their_rows():
+    c = Call(17, [4, 1], [90, 90])
+    c.qkv_d[1, 70] = float("inf")
+    c.qkv_d[2, 3] = float("nan")
+    c.upload()
+    out, ws = c.attend()
+    torch.cuda.synchronize()
+    bad = torch.isnan(out.view(5, 8, 64)).all(-1).cpu().numpy()
+    want = np.zeros((5, 8), bool)
+    want[1, 1] = want[2, 0] = True
+    assert np.array_equal(bad, want)
+
+
+def test_attention_bad_page_is_reported():
+    c = Call(18, [1, 2], [300, 10])
+    good = c.table.copy()
+    for bad in (-1, c.num_pages, 2 ** 31 - 1, -2 ** 31):
+        c.table = good.copy()
+        c.table[0, 2] = bad
+        c.upload()
+        _, ws = c.attend()
+        torch.cuda.synchronize()
+        assert ptl.last_device_error(ws) == ptl.STATUS_CODE["PTL_ERR_BAD_PAGE"]
+        # outside the window it is not needed
+        out, ws = c.attend(window=70, sinks=20)
+        torch.cuda.synchronize()
+        assert ptl.last_device_error(ws) == 0 and torch.isfinite(out).all()
+
+
+def test_two_users_of_a_call_share_pages():
+    c = Call(19, [3, 3], [200, 200])
+    c.table[1] = c.table[0]
+    c.qkv_d[3:] = c.qkv_d[:3]
+    c.upload()
+    out = c.check()
+    assert torch.equal(out[:3], out[3:])
+
+
+# ------------------------------------------------------ streams and graphs
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_same_bits_on_other_streams_and_in_graphs(dt):
+    """Two calls under way at once, each with its workspace; two graphs that
+    share one, replayed in turn, on new inputs."""
+    a, b = Call(20, [1, 7, 90], [4000, 50, 0], dt), Call(21, [2, 1, 33], [10, 9000, 200], dt)
+    want = [c.check().clone() for c in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    wss = [ptl.attention_paged_workspace(c.T, 3, dt) for c in (a, b)]
+    outs = [torch.zeros(c.T, 512, dtype=tdt(dt), device="cuda") for c in (a, b)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s, ws, o in zip((a, b), streams, wss, outs):
+            c.attend(ws=ws, out=o, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    graphs = []
+    small = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    for c, o in zip((a, b), outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.append(ws=small)
+            c.attend(ws=wss[0], out=o)
+        graphs.append(g)
+    for _ in range(3):
+        for c in (a, b):
+            c.qkv_d.normal_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for c, o in zip((a, b), outs):
+            got = o.clone()
+            c.qkv = host(c.qkv_d)
+            assert torch.equal(got, c.check())
+    assert ptl.last_device_error(wss[0]) == 0 and ptl.last_device_error(small) == 0
+
+
+# ------------------------------------------------------------- page copy
+@pytest.mark.parametrize("pairs", [[(0, 1)], [(3, 0), (3, 5), (4, 1)], [(i, 39 - i) for i in range(20)]])
+def test_copy_pages(pairs):
+    rng = np.random.default_rng(len(pairs))
+    codes, scales = make_pages(rng, 40)
+    kv = ptl.KvPages(dev(codes, torch.uint8), dev(scales, torch.float32))
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    src, dst = (dev(np.array(x), torch.int32) for x in zip(*pairs))
+    ptl.kv_copy_pages(kv, src, dst, ws)
+    torch.cuda.synchronize()
+    assert ptl.last_device_error(ws) == 0
+    for s, d in pairs:
+        codes[d], scales[d] = codes[s], scales[s]
+    assert np.array_equal(kv.codes.cpu().numpy(), codes) and np.array_equal(kv.scales.cpu().numpy(), scales)
+
+
+def test_copy_skips_and_reports_bad_pages():
+    rng = np.random.default_rng(1)
+    codes, scales = make_pages(rng, 4)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    for s, d in [(-1, 1), (4, 1), (0, -1), (0, 4), (2 ** 31 - 1, -2 ** 31)]:
+        kv = ptl.KvPages(dev(codes, torch.uint8), dev(scales, torch.float32))
+        ptl.kv_copy_pages(kv, dev(np.array([s, 2]), torch.int32), dev(np.array([d, 3]), torch.int32), ws)
+        torch.cuda.synchronize()
+        assert ptl.last_device_error(ws) == ptl.STATUS_CODE["PTL_ERR_BAD_PAGE"]
+        want = codes.copy()
+        want[3] = codes[2]
+        assert np.array_equal(kv.codes.cpu().numpy(), want)
+
+
+# ------------------------------------------------------------- together
+def test_served_sequences_fork_trim_and_compact():
+    """Prompts, single tokens, forks that go different ways, a window with
+    pages given up, released sequences and a compaction: the attention of each
+    step against the oracle on what the append holds for each sequence alone."""
+    rng = np.random.default_rng(30)
+    pool, kv = ptl.KvPool(64, 12), ptl.alloc_kv_pages(64)
+    small = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    ws = ptl.attention_paged_workspace(2000, 12, "bf16")
+    # the same sequences, each in pages of its own that are never shared or moved
+    own_v, own_s = np.zeros((12 * 20, 2, 8, 64, 64)), np.zeros((12 * 20, 2, 8))
+    own_table = np.arange(12 * 20).reshape(12, 20)
+
+    def step(seqs, new, window=0, sinks=0):
+        past = [pool.length(q) for q in seqs]
+        pool.reserve(seqs, [p + n for p, n in zip(past, new)])
+        cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        qkv = dev(rng.standard_normal((int(cu[-1]), 1536)).astype(np.float32), torch.bfloat16)
+        table = pool.table(seqs).cuda()
+        cu_d, past_d = dev(cu, torch.int32), dev(np.array(past), torch.int32)
+        out = torch.empty(int(cu[-1]), 512, dtype=torch.bfloat16, device="cuda")
+        ptl.kv_append(qkv, cu_d, kv, table, past_d, small)
+        ptl.attention_paged(qkv, out, cu_d, kv, table, past_d, ws, window=window, sinks=sinks)
+        torch.cuda.synchronize()
+        assert ptl.last_device_error(small) == 0 and ptl.last_device_error(ws) == 0
+        x = host(qkv)
+        O.kv_append(own_v, own_s, x[:, 512:].reshape(-1, 2, 8, 64), cu, own_table[seqs], past)
+        ref, mag, smax, count = O.attention_paged(x[:, :512].reshape(-1, 8, 64), own_v, own_s, cu, own_table[seqs],
+                                                  past, window, sinks, details=True)
+        c = Call.__new__(Call)
+        c.dt, c.kv = "bf16", kv
+        off = np.abs(host(out).reshape(ref.shape) - ref) - c.bound(ref, mag, smax, count)
+        assert (off <= 0).all(), float(off.max())
+
+    def copy(lists):
+        src, dst = lists
+        ptl.kv_copy_pages(kv, src.cuda(), dst.cuda(), small)
+
+    step([0, 1, 2], [200, 64, 37])
+    step([2, 0, 1], [1, 1, 1])
+    src, dst = pool.fork([0, 0, 1, 2], [3, 4, 5, 6])
+    assert len(src) == 4
+    copy((src, dst))
+    for s, d in zip([0, 0, 1, 2], [3, 4, 5, 6]):
+        own_v[own_table[d]], own_s[own_table[d]] = own_v[own_table[s]], own_s[own_table[s]]
+    step([0, 3, 4, 5, 6], [1, 5, 80, 1, 30])
+    step([0, 1, 2, 3, 4, 5, 6], [1] * 7)
+    pool.release([1, 4])
+    free = pool.free_pages
+    assert pool.trim([0, 3], 70, 10) > 0 and pool.free_pages > free
+    copy(pool.compact())
+    used = 64 - pool.free_pages
+    assert int(pool.table([0, 2, 3, 5, 6], 20).max()) == used - 1
+    step([0, 3], [3, 1], window=70, sinks=10)
+    for q in (1, 4):
+        own_v[own_table[q]], own_s[own_table[q]] = 0.0, 0.0
+    step([2, 5, 6, 1], [1, 2, 100, 66])
+    pool.release(range(12))
+    assert pool.free_pages == 64
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_layer_over_the_cache(dt):
+    """One encoder layer served from the cache, step entry point by step entry
+    point: with a fresh cache its attention differs from the layer's own only
+    by the keys' and values' rounding to e4m3; the rest of the layer is the
+    same calls."""
+    case = S.make_case(f"kv_{dt}", lengths=[70, 3, 0, 129], seed=4, dtype=dt, gate_std=0.1, random_bias=True)
+    T, U = case.total_tokens, case.num_users
+    td = tdt(dt)
+    w = ptl.to_device_layer(case.layers[0], dt)
+    x, cu = dev(case.x, td), dev(case.cu_seqlens, torch.int32)
+    ws, pws = ptl.alloc_workspace(T, U, dt), ptl.attention_paged_workspace(T, U, dt)
+    pool, kv = ptl.KvPool(8, U), ptl.alloc_kv_pages(8)
+    pool.reserve(range(U), case.lengths.tolist())
+    table, past = pool.table(range(U)).cuda(), torch.zeros(U, dtype=torch.int32, device="cuda")
+
+    def layer(x, cu, table, past):
+        t = x.shape[0]
+        qkv, attn = torch.empty(t, 1536, dtype=td, device="cuda"), torch.empty(t, 512, dtype=td, device="cuda")
+        x1, out = torch.empty(t, 512, device="cuda"), torch.empty(t, 512, dtype=td, device="cuda")
+        xn2 = torch.empty(t, 512, dtype=td, device="cuda")
+        idx = torch.empty(t, 2, dtype=torch.int32, device="cuda")
+        tw = torch.empty(t, 2, device="cuda")
+        ptl.qkv_projection(x, qkv, w, ws)
+        ptl.kv_append(qkv, cu, kv, table, past, pws)
+        ptl.attention_paged(qkv, attn, cu, kv, table, past, pws)
+        ptl.out_projection(attn, x, x1, w, ws)
+        ptl.gate(x1, xn2, idx, tw, w, ws)
+        ptl.moe(xn2, idx, tw, x1, out, w, ws)
+        torch.cuda.synchronize()
+        assert ptl.last_device_error(ws) == 0 and ptl.last_device_error(pws) == 0
+        return qkv, attn, out
+
+    qkv, attn, out = layer(x, cu, table, past)
+    h = host(qkv)
+    vals, sc = np.zeros((8, 2, 8, 64, 64)), np.ones((8, 2, 8))
+    O.kv_append(vals, sc, h[:, 512:].reshape(T, 2, 8, 64), case.cu_seqlens, table.cpu().numpy(), [0] * U)
+    ref, mag, smax, count = O.attention_paged(h[:, :512].reshape(T, 8, 64), vals, sc, case.cu_seqlens,
+                                              table.cpu().numpy(), [0] * U, details=True)
+    c = Call.__new__(Call)
+    c.dt, c.kv = dt, kv
+    assert (np.abs(host(attn).reshape(ref.shape) - ref) <= c.bound(ref, mag, smax, count)).all()
+    assert torch.isfinite(out).all()
+    # the last token of each user served as a step of its own: the same codes
+    # already stand in the pages, so it is the row that the prompt gave
+    users = [0, 1, 3]
+    rows = [int(case.cu_seqlens[u + 1]) - 1 for u in users]
+    one = layer(x[rows].contiguous(), torch.arange(4, dtype=torch.int32, device="cuda"),
+                table[users].contiguous(), dev(np.array([case.lengths[u] - 1 for u in users]), torch.int32))
+    b = c.bound(ref, mag, smax, count)[rows]
+    assert (np.abs(host(one[1]).reshape(3, 8, 64) - ref[rows]) <= b).all()
