@@ -23,7 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libptl.so")
 SOURCES = ["api.cu", "kernels_simt.cu", "gemm_tc.cu", "attn_tc.cu", "noalloc.cu", "runner.cu", "partition.cu",
-           "kv_pool.cu", "kv_cache.cu", "attn_paged.cu"]
+           "kv_pool.cu", "kv_cache.cu", "attn_paged.cu", "attn_paged_tc.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-Xptxas", "-v"]

@@ -850,7 +850,7 @@ ptl_status ptl_kv_copy_pages(const ptl_kv_pages* kv, const int32_t* src, const i
 // The paged attention's workspace: the error word, the split units' counters
 // (cleared together by each call), the split units' parts.
 static constexpr size_t kPagedCounters = 256;
-static constexpr size_t kPagedClear = kPagedCounters + sizeof(int32_t) * PAGED_MAX_CTAS * H;
+static constexpr size_t kPagedClear = kPagedCounters + sizeof(int32_t) * (PAGED_MAX_CTAS * H + 2 * PAGED_TC_MAX_CTAS);
 
 size_t ptl_attention_paged_workspace_size(int64_t max_tokens, int32_t max_users, ptl_dtype dt) {
   if (max_tokens < 0 || max_tokens >= (int64_t(1) << 31) || max_users < 1 || (dt != PTL_F32 && dt != PTL_BF16)) return 0;
@@ -884,7 +884,7 @@ ptl_status ptl_attention_paged(const void* qkv, void* attn, const int32_t* cu_se
   const PagedArgs a{qkv, attn, cu_seqlens, page_table, past_lens, kv->codes, kv->scales,
                     reinterpret_cast<int32_t*>(ws), reinterpret_cast<int32_t*>(ws + kPagedCounters),
                     reinterpret_cast<float*>(ws + align_up(kPagedClear, 256)), kv->num_pages, max_pages, num_users,
-                    int(total_tokens), window, sinks};
+                    int(total_tokens), window, sinks, 0};
   PTL_TRY(launch_attn_paged(a, dt, st));
   return PTL_OK;
 }

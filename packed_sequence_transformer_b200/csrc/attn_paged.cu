@@ -104,7 +104,7 @@ struct PagedWalk {
       do {
         ++u;
         load(a);
-      } while (n == 0);
+      } while (n == 0 || n > a.few);
     }
     see(a);
   }
@@ -113,6 +113,7 @@ struct PagedWalk {
 // Steps of one user.
 __device__ __forceinline__ int64_t paged_user_steps(const PagedArgs& a, int n, int past) {
   int64_t s = 0;
+  if (n > a.few) return 0;
   for (int q0 = 0; q0 < n; q0 += PA_QG)
     s += page_span(past + q0, past + min(q0 + PA_QG, n) - 1, a.window, a.sinks).count;
   return s;
@@ -548,10 +549,16 @@ static int launch_paged_t(const PagedArgs& a, cudaStream_t st) {
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
-size_t paged_partial_bytes() { return sizeof(float) * 2 * PAGED_MAX_CTAS * H * PA_PART; }
+size_t paged_partial_bytes() {
+  const size_t few = sizeof(float) * 2 * PAGED_MAX_CTAS * H * PA_PART;
+  return few > paged_tc_partial_bytes() ? few : paged_tc_partial_bytes();  // one launch after the other
+}
 
-int launch_attn_paged(const PagedArgs& a, ptl_dtype dt, cudaStream_t st) {
-  return dt == PTL_BF16 ? launch_paged_t<__nv_bfloat16, 1>(a, st) : launch_paged_t<float, 2>(a, st);
+int launch_attn_paged(PagedArgs a, ptl_dtype dt, cudaStream_t st) {
+  a.few = dt == PTL_BF16 ? PAGED_FEW : INT32_MAX;
+  const int r = dt == PTL_BF16 ? launch_paged_t<__nv_bfloat16, 1>(a, st) : launch_paged_t<float, 2>(a, st);
+  if (r != 0 || dt != PTL_BF16 || a.T <= PAGED_FEW) return r;
+  return launch_attn_paged_tc(a, st);
 }
 
 }  // namespace ptl

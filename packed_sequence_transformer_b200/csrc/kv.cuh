@@ -20,6 +20,8 @@ constexpr int KV_TILE = KV_PAGE * DH;       // bytes of one side of one head of 
 constexpr int KV_SIDE = H * KV_TILE;        // bytes of the keys (or the values) of a page
 constexpr int KV_PAGE_BYTES = 2 * KV_SIDE;  // 65536
 constexpr int KV_MIN_EXP = -100;            // smallest scale 2^-100
+constexpr int PAGED_FEW = 32;
+constexpr int PAGED_TC_MAX_CTAS = 148;
 constexpr int PAGED_MAX_CTAS = 2 * 148;     // bound on the paged attention's grid (its workspace holds two parts per block)
 constexpr int KV_MAX_PAGES = (1 << 25) - 1;  // pages of a sequence: positions stay below 2^31
 
@@ -42,6 +44,7 @@ struct PagedArgs {
   int32_t* counters;  // [CTA][head] parts of a split unit done so far
   float* partial;     // [2 CTA + which][head] unfinished sums of split units
   int num_pages, max_pages, U, T, window, sinks;
+  int few;            // users with more new tokens go to the tcgen05 kernel
 };
 
 // One user's place in a call, checked: n new tokens behind `past` kept ones.
@@ -61,6 +64,10 @@ __device__ __forceinline__ int kv_check_user(const int32_t* cu, const int32_t* p
 struct PageSpan {
   int sinks, first, count;
   __device__ __forceinline__ int page(int k) const { return k < sinks ? k : first + k - sinks; }
+  // of the first page of the span that is not below `page`
+  __device__ __forceinline__ int place(int page) const {
+    return page < sinks ? page : page < first ? sinks : page - first + sinks;
+  }
 };
 __device__ __forceinline__ PageSpan page_span(int p0, int p1, int window, int sinks) {
   PageSpan s{0, 0, (p1 >> 6) + 1};

@@ -182,7 +182,10 @@ int launch_kv_copy(uint8_t* codes, float* scales, int num_pages, const int32_t* 
                    int32_t* err, cudaStream_t st);
 // attn_paged.cu: attention over the paged cache (the counters must be zero)
 size_t paged_partial_bytes();
-int launch_attn_paged(const PagedArgs& a, ptl_dtype dt, cudaStream_t st);
+int launch_attn_paged(PagedArgs a, ptl_dtype dt, cudaStream_t st);
+// attn_paged_tc.cu: the users with more than a.few new tokens
+size_t paged_tc_partial_bytes();
+int launch_attn_paged_tc(const PagedArgs& a, cudaStream_t st);
 
 // attn_tc.cu (bf16, tcgen05)
 // mask (nullable): the HSTU-style variant, over a work list built with the

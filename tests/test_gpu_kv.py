@@ -161,6 +161,8 @@ def test_attention_many_parts(dt):
     Call(11, [1], [20000], dt).check()
     Call(12, [2, 1, 9, 1], [9000, 10, 4000, 12345], dt).check()
     Call(13, [1, 1], [15000, 15000], dt).check(window=9000, sinks=70)
+    Call(31, [40], [12000], dt).check()
+    Call(32, [50, 140, 33], [5000, 3000, 0], dt).check(window=2900, sinks=100)
 
 
 def test_attention_many_users():
@@ -170,11 +172,12 @@ def test_attention_many_users():
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
-def test_attention_magnitudes(dt):
+@pytest.mark.parametrize("new", [[16, 6], [150, 40]])
+def test_attention_magnitudes(dt, new):
     """Rows of q from tiny to huge, scales far apart from page to page."""
-    c = Call(15, [16, 6], [200, 300], dt)
+    c = Call(15, new, [200, 300], dt)
     x = host(c.qkv_d).astype(np.float32)
-    x[:, :512] *= (10.0 ** np.linspace(-30, 1, 22))[:, None].astype(np.float32)
+    x[:, :512] *= (10.0 ** np.linspace(-30, 1, c.T))[:, None].astype(np.float32)
     x[3, :512] = 0.0
     c.qkv_d = dev(x, tdt(dt))
     c.scales[:, 1] *= (2.0 ** c.rng.integers(-30, 20, (c.num_pages, 8))).astype(np.float32)
