@@ -43,6 +43,7 @@ using namespace sm100;
 
 constexpr int PA_THREADS = 32 * H;
 constexpr int PA_QG = 8;        // queries of a unit
+constexpr int PA_PARTS = 128;   // blocks that share a unit, at most about
 constexpr int PA_STAGES = 3;    // 4 KB tiles in a warp's ring
 constexpr int PA_SMEM = H * PA_STAGES * KV_TILE;
 constexpr int PA_PART = PA_QG * (DH + 2);  // floats of one head's part: O, then (m, l) per query
@@ -77,6 +78,11 @@ __device__ __forceinline__ uint32_t pack_rest2(float lo, float hi, uint32_t firs
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&first));
   return pack_half2(lo - f.x, hi - f.y);
 }
+
+template <int N>
+struct Count {
+  static constexpr int value = N;
+};
 
 // A position in the call's (unit, page) steps.
 struct PagedWalk {
@@ -124,7 +130,9 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
   extern __shared__ __align__(128) uint8_t ring_all[];
   __shared__ uint64_t s_bar[H][PA_STAGES];
   __shared__ int64_t s_scan[H];
+  __shared__ int s_longest[H];
   __shared__ int s_first[3];
+  __shared__ PagedWalk s_walk[H][2];
   __shared__ int64_t s_start;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int head = warp, g = lane >> 2, t = lane & 3;
@@ -141,12 +149,16 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
   const int per = (a.U + PA_THREADS - 1) / PA_THREADS;
   const int u_lo = min(tid * per, a.U), u_hi = min(u_lo + per, a.U);
   int64_t mine = 0;
+  int longest = 0;  // pages of the longest unit
   int bad = 0;
   for (int u = u_lo; u < u_hi; ++u) {
     int n, p;
     const int e = kv_check_user(a.cu, a.past, u, a.U, a.T, a.max_pages, n, p);
     bad |= e == 0 ? 0 : e == PTL_ERR_BAD_OFFSETS ? 1 : 2;
-    if (e == 0) mine += paged_user_steps(a, n, p);
+    if (e == 0 && n > 0 && n <= a.few) {
+      mine += paged_user_steps(a, n, p);
+      longest = max(longest, page_span(p + (n - 1) / PA_QG * PA_QG, p + n - 1, a.window, a.sinks).count);
+    }
   }
   if (__syncthreads_or(bad)) {  // every block sees the same offsets: nothing is written
     const int offsets = __syncthreads_or(bad & 1);
@@ -159,16 +171,23 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
     const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) s_scan[warp] = incl;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) {
+    s_scan[warp] = incl;
+    s_longest[warp] = longest;
+  }
   __syncthreads();
   int64_t base = incl - mine, W = 0;
 #pragma unroll
   for (int w = 0; w < H; ++w) {
     if (w < warp) base += s_scan[w];
     W += s_scan[w];
+    longest = max(longest, s_longest[w]);
   }
-  // this block's steps [A, B)
-  const int64_t G = W < int64_t(gridDim.x) ? W : int64_t(gridDim.x);
+  // this block's steps [A, B); so few blocks that no unit falls into more than
+  // PA_PARTS (one block adds them up)
+  int64_t G = W < int64_t(gridDim.x) ? W : int64_t(gridDim.x);
+  if (longest > PA_PARTS && G * longest > PA_PARTS * W) G = PA_PARTS * W / longest;
   if (int64_t(blockIdx.x) >= G) return;
   const int64_t A = blockIdx.x * W / G, B = (blockIdx.x + 1) * W / G;
   if (A >= base && A < base + mine) {
@@ -196,44 +215,52 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
   }
   __syncthreads();
 
-  PagedWalk cw;  // the step being computed
-  cw.u = s_first[0];
-  cw.q0 = s_first[1];
-  cw.k = s_first[2];
-  cw.start = s_start;
-  cw.load(a);
-  cw.see(a);
-  PagedWalk iw = cw;  // the step whose tiles are loaded next
+  // The step being computed and the step whose tiles are loaded next live in
+  // shared memory (a warp's own; lane 0 moves them on): the loop needs the
+  // registers.
+  PagedWalk& cw = s_walk[warp][0];
+  PagedWalk& iw = s_walk[warp][1];
+  if (lane == 0) {
+    cw.u = s_first[0];
+    cw.q0 = s_first[1];
+    cw.k = s_first[2];
+    cw.start = s_start;
+    cw.load(a);
+    cw.see(a);
+    iw = cw;
+  }
+  __syncwarp();
   const int64_t steps = B - A;
 
-  // tiles are loaded in the order K0 V0 K1 V1 ...; a stage's phase flips each time round
+  // tiles are loaded in the order K0 V0 K1 V1 ..., by lane 0; a stage's phase
+  // flips each time round
   int64_t sent = 0, used = 0;
   int st_i = 0, st_c = 0, ph_c = 0;
-  int id = 0, id_next = iw.entry(a);
-  float ks0 = 0.f, ks1 = 0.f, vs0 = 0.f, vs1 = 0.f;  // scales of the pages under way, by parity
+  int id = 0, id_next = lane == 0 ? iw.entry(a) : 0;
+  float ks0 = 0.f, ks1 = 0.f, vs0 = 0.f, vs1 = 0.f;  // lane 0: scales of the pages under way, by parity
   auto issue = [&]() {
     if (sent >= 2 * steps) return;
-    const bool key = (sent & 1) == 0;
-    if (key) {
-      id = id_next;
-      if (id < 0 || id >= a.num_pages) {  // reported; page 0 stands in, the output is undefined
-        if (lane == 0) set_error(a.err, PTL_ERR_BAD_PAGE);
-        id = 0;
-      }
-      const float* sc = a.scales + int64_t(id) * 2 * H + head;
-      if ((sent >> 1) & 1) {
-        ks1 = __ldg(sc);
-        vs1 = __ldg(sc + H);
-      } else {
-        ks0 = __ldg(sc);
-        vs0 = __ldg(sc + H);
-      }
-      if ((sent >> 1) + 1 < steps) {
-        iw.next(a);
-        id_next = iw.entry(a);
-      }
-    }
     if (lane == 0) {
+      const bool key = (sent & 1) == 0;
+      if (key) {
+        id = id_next;
+        if (id < 0 || id >= a.num_pages) {  // reported; page 0 stands in, the output is undefined
+          set_error(a.err, PTL_ERR_BAD_PAGE);
+          id = 0;
+        }
+        const float* sc = a.scales + int64_t(id) * 2 * H + head;
+        if ((sent >> 1) & 1) {
+          ks1 = __ldg(sc);
+          vs1 = __ldg(sc + H);
+        } else {
+          ks0 = __ldg(sc);
+          vs0 = __ldg(sc + H);
+        }
+        if ((sent >> 1) + 1 < steps) {
+          iw.next(a);
+          id_next = iw.entry(a);
+        }
+      }
       mbar_arrive_expect_tx(&bar[st_i], KV_TILE);
       bulk_load(ring + st_i * KV_TILE, a.codes + int64_t(id) * KV_PAGE_BYTES + (key ? 0 : KV_SIDE) + head * KV_TILE,
                 KV_TILE, &bar[st_i]);
@@ -290,7 +317,8 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
     }
-    const float ks = (i & 1) ? ks1 : ks0, vs = (i & 1) ? vs1 : vs0;
+    const float ks = __shfl_sync(0xffffffffu, (i & 1) ? ks1 : ks0, 0);
+    const float vs = __shfl_sync(0xffffffffu, (i & 1) ? vs1 : vs0, 0);
 
     // S = K Q^T: row r of tile mt is token 16 (r / 2 % 4) + 4 mt + 2 (r / 8) + r % 2
     if (!mbar_wait(&bar[st_c], ph_c)) {
@@ -484,38 +512,77 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
         done = __shfl_sync(0xffffffffu, done, 0);
         if (done == c1 - c0) {  // the last part: add them up, in block order
           __threadfence();
-          for (int q = 0; q < nq; ++q) {
-            float M = -INFINITY;
-            for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(part(c) + PA_QG * DH + 2 * q));
+          // four lanes a query: maximum and sum over all parts
+          const int q4 = lane >> 2;
+          float M = -INFINITY, L = 0.f;
+#pragma unroll 4
+          for (int c = c0 + (lane & 3); c <= c1; c += 4) {
+            if (q4 < nq) {
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(c) + PA_QG * DH + 2 * q4));
+              const float mn = fmaxf(M, ml.x);
+              if (mn != -INFINITY) L = ex2_approx(M - mn) * L + ex2_approx(ml.x - mn) * ml.y;
+              M = mn;
+            }
+          }
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-            if (M == -INFINITY) M = 0.f;
-            float L = 0.f, x0 = 0.f, x1 = 0.f;
-            for (int cb = c0; cb <= c1; cb += 32) {
-              float w = 0.f;
-              if (cb + lane <= c1) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(cb + lane) + PA_QG * DH + 2 * q));
-                w = ex2_approx(ml.x - M);
-                L += w * ml.y;
-              }
-              const int cnt = min(32, c1 - cb + 1);
-#pragma unroll 8
-              for (int e = 0; e < cnt; ++e) {
-                const float we = __shfl_sync(0xffffffffu, w, e);
-                const float2 v = __ldcg(reinterpret_cast<const float2*>(part(cb + e) + q * DH + 2 * lane));
-                x0 = fmaf(we, v.x, x0);
-                x1 = fmaf(we, v.y, x1);
+          for (int off = 1; off < 4; off <<= 1) {
+            const float Mo = __shfl_xor_sync(0xffffffffu, M, off), Lo = __shfl_xor_sync(0xffffffffu, L, off);
+            const float mn = fmaxf(M, Mo);
+            if (mn != -INFINITY) L = ex2_approx(M - mn) * L + ex2_approx(Mo - mn) * Lo;
+            M = mn;
+          }
+          if (M == -INFINITY) M = 0.f;
+          const float inv = 1.0f / L;
+          // 16 lanes hold a row, the two halves of the warp take parts in turn
+          const int half = lane >> 4, d4 = lane & 15;
+          auto add_up = [&](auto rows, auto depth, int q0) {
+            constexpr int NQ = decltype(rows)::value, UN = decltype(depth)::value;
+            float4 acc[NQ];
+            float Mq[NQ];
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+              acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+              Mq[q] = __shfl_sync(0xffffffffu, M, 4 * min(q0 + q, PA_QG - 1));
+            }
+#pragma unroll UN
+            for (int c = c0 + half; c <= c1; c += 2) {
+              const float* pc = part(c);
+#pragma unroll
+              for (int q = 0; q < NQ; ++q) {
+                if (q0 + q >= nq) continue;
+                const float we = ex2_approx(__ldcg(pc + PA_QG * DH + 2 * (q0 + q)) - Mq[q]);
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(pc + (q0 + q) * DH) + d4);
+                acc[q].x = fmaf(we, v.x, acc[q].x);
+                acc[q].y = fmaf(we, v.y, acc[q].y);
+                acc[q].z = fmaf(we, v.z, acc[q].z);
+                acc[q].w = fmaf(we, v.w, acc[q].w);
               }
             }
-            L = warp_sum(L);
-            const float inv = 1.0f / L;
-            dst[q * D + 2 * lane] = from_f32<T>(x0 * inv);
-            dst[q * D + 2 * lane + 1] = from_f32<T>(x1 * inv);
-          }
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+              const float iq = __shfl_sync(0xffffffffu, inv, 4 * min(q0 + q, PA_QG - 1));
+              float o4[4] = {acc[q].x, acc[q].y, acc[q].z, acc[q].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o4[e] = (o4[e] + __shfl_xor_sync(0xffffffffu, o4[e], 16)) * iq;
+              if (half == 0 && q0 + q < nq) {
+                T* d = dst + (q0 + q) * D + 4 * d4;
+                if constexpr (sizeof(T) == 2)
+                  *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16x2(o4[0], o4[1]), pack_bf16x2(o4[2], o4[3]));
+                else
+                  *reinterpret_cast<float4*>(d) = make_float4(o4[0], o4[1], o4[2], o4[3]);
+              }
+            }
+          };
+          if (nq == 1)
+            add_up(Count<1>{}, Count<8>{}, 0);
+          else
+            for (int q0 = 0; q0 < nq; q0 += 4) add_up(Count<4>{}, Count<2>{}, q0);
         }
       }
     }
-    if (i + 1 < steps) cw.next(a);
+    __syncwarp();
+    if (lane == 0 && i + 1 < steps) cw.next(a);
+    __syncwarp();
   }
   if (!ok) {
     set_error(a.err, PTL_ERR_TIMEOUT);

@@ -9,7 +9,6 @@ raises; there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Dict, Iterable, List, Optional
@@ -223,10 +222,36 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
-def _on(t: torch.Tensor):
-    """The device of a call's tensors, as the current one (CPU tensors: as it is,
-    the library then refuses or returns without work)."""
-    return torch.cuda.device(t.device) if t.is_cuda else contextlib.nullcontext()
+class _On:
+    """The device of a call's tensors as the current one, and the stream to use
+    there: the caller's, or that device's current stream.  CPU tensors leave
+    both as they are (the library then refuses or returns without work).  A
+    call on the paged cache may be one small kernel, so this is written to
+    cost less than launching it: torch's device guard and stream objects are
+    made only where they are needed."""
+    __slots__ = ("index", "guard")
+
+    def __init__(self, t: torch.Tensor):
+        self.index = t.device.index if t.is_cuda else -1
+        self.guard = None
+
+    def __enter__(self):
+        if self.index >= 0 and torch.cuda.current_device() != self.index:
+            self.guard = torch.cuda.device(self.index)
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+    def stream(self, stream):
+        if stream is None and self.index >= 0:
+            return torch._C._cuda_getCurrentRawStream(self.index)
+        if isinstance(stream, torch.cuda.Stream):
+            return stream.cuda_stream
+        return int(stream or 0)
 
 
 def torch_dtype(dt) -> torch.dtype:
@@ -457,6 +482,7 @@ class KvPages:
             raise ValueError("codes and scales must be on one device")
         self.codes, self.scales = codes, scales
         self._struct = KvPagesStruct(_ptr(codes), _ptr(scales), n)
+        self._ref = ctypes.byref(self._struct)
 
 
 def alloc_kv_pages(num_pages: int, device="cuda") -> KvPages:
@@ -465,32 +491,42 @@ def alloc_kv_pages(num_pages: int, device="cuda") -> KvPages:
                    torch.ones(num_pages, 2, 8, dtype=torch.float32, device=device))
 
 
+_I32, _U8 = torch.int32, torch.uint8
+
+
 def _check_paged(qkv, cu_seqlens, kv: KvPages, page_table, past_lens, workspace, attn=None):
-    """Shapes, types and devices of a call on the paged cache; its users and table width."""
-    users = past_lens.numel()
-    if qkv.dim() != 2 or qkv.shape[1] != 1536:
+    """Shapes, types, layout and devices of a call on the paged cache; its rows,
+    users and table width."""
+    T, width = qkv.shape
+    users, max_pages = page_table.shape
+    dev = qkv.device
+    if width != 1536:
         raise ValueError("qkv must be [T, 1536]")
-    if attn is not None and (tuple(attn.shape) != (qkv.shape[0], 512) or attn.dtype != qkv.dtype):
-        raise ValueError("attn must be [T, 512] of qkv's dtype")
-    if cu_seqlens.numel() != users + 1 or page_table.dim() != 2 or page_table.shape[0] != users:
+    if past_lens.shape != (users,) or cu_seqlens.shape != (users + 1,):
         raise ValueError("cu_seqlens [U + 1], page_table [U, max_pages] and past_lens [U] do not agree")
-    for t in (cu_seqlens, page_table, past_lens):
-        if t.dtype != torch.int32:
-            raise ValueError("cu_seqlens, page_table and past_lens must be int32")
-    for t in (cu_seqlens, kv.codes, page_table, past_lens, workspace) + (() if attn is None else (attn,)):
-        if t.device != qkv.device:
+    if cu_seqlens.dtype is not _I32 or page_table.dtype is not _I32 or past_lens.dtype is not _I32:
+        raise ValueError("cu_seqlens, page_table and past_lens must be int32")
+    if attn is not None and (attn.shape != (T, 512) or attn.dtype is not qkv.dtype):
+        raise ValueError("attn must be [T, 512] of qkv's dtype")
+    for t in (qkv, cu_seqlens, page_table, past_lens, workspace) if attn is None else (
+            qkv, cu_seqlens, page_table, past_lens, workspace, attn):
+        if not t.is_contiguous():
+            raise ValueError("tensors passed to libptl must be contiguous")
+        if t.device != dev:
             raise ValueError("all tensors of a call must be on one device")
-    return users, page_table.shape[1]
+    if kv.codes.device != dev:
+        raise ValueError("all tensors of a call must be on one device")
+    return T, users, max_pages
 
 
 def kv_append(qkv, cu_seqlens, kv: KvPages, page_table, past_lens, workspace, stream=None):
     """ptl_kv_append: the keys and values of qkv [T, 1536] into the pages, token
     i of user u at position past_lens[u] + i.  workspace: >= 256 bytes."""
-    U, max_pages = _check_paged(qkv, cu_seqlens, kv, page_table, past_lens, workspace)
-    with _on(qkv):
-        _check(lib().ptl_kv_append(_ptr(qkv), _ptr(cu_seqlens), U, qkv.shape[0], _dt(qkv.dtype),
-                                   ctypes.byref(kv._struct), _ptr(page_table), max_pages, _ptr(past_lens),
-                                   _ptr(workspace), workspace.numel(), _stream(stream)), "ptl_kv_append")
+    T, U, max_pages = _check_paged(qkv, cu_seqlens, kv, page_table, past_lens, workspace)
+    with _On(qkv) as on:
+        _check(lib().ptl_kv_append(qkv.data_ptr(), cu_seqlens.data_ptr(), U, T, _dt(qkv.dtype), kv._ref,
+                                   page_table.data_ptr(), max_pages, past_lens.data_ptr(), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), on.stream(stream)), "ptl_kv_append")
     return kv
 
 
@@ -506,12 +542,12 @@ def attention_paged(qkv, attn, cu_seqlens, kv: KvPages, page_table, past_lens, w
     """ptl_attention_paged: the new tokens' attention over the pages (which
     hold the new tokens too), causal, with window > 0 only the last `window`
     keys and the sequence's first `sinks`, into attn [T, 512]."""
-    U, max_pages = _check_paged(qkv, cu_seqlens, kv, page_table, past_lens, workspace, attn)
-    with _on(qkv):
-        _check(lib().ptl_attention_paged(_ptr(qkv), _ptr(attn), _ptr(cu_seqlens), U, qkv.shape[0], _dt(qkv.dtype),
-                                         ctypes.byref(kv._struct), _ptr(page_table), max_pages, _ptr(past_lens),
-                                         int(window), int(sinks), _ptr(workspace), workspace.numel(),
-                                         _stream(stream)), "ptl_attention_paged")
+    T, U, max_pages = _check_paged(qkv, cu_seqlens, kv, page_table, past_lens, workspace, attn)
+    with _On(qkv) as on:
+        _check(lib().ptl_attention_paged(qkv.data_ptr(), attn.data_ptr(), cu_seqlens.data_ptr(), U, T, _dt(qkv.dtype),
+                                         kv._ref, page_table.data_ptr(), max_pages, past_lens.data_ptr(), window,
+                                         sinks, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                         on.stream(stream)), "ptl_attention_paged")
     return attn
 
 
@@ -520,11 +556,14 @@ def kv_copy_pages(kv: KvPages, src, dst, workspace, stream=None):
     ``KvPool.fork`` and ``KvPool.compact`` give them).  workspace: >= 256 bytes."""
     if src.dtype != torch.int32 or dst.dtype != torch.int32 or src.shape != dst.shape or src.dim() != 1:
         raise ValueError("src and dst must be int32 lists of one length")
+    if not (src.is_contiguous() and dst.is_contiguous() and workspace.is_contiguous()):
+        raise ValueError("tensors passed to libptl must be contiguous")
     if any(t.device != kv.codes.device for t in (src, dst, workspace)):
         raise ValueError("all tensors of a call must be on one device")
-    with _on(kv.codes):
-        _check(lib().ptl_kv_copy_pages(ctypes.byref(kv._struct), _ptr(src), _ptr(dst), src.numel(), _ptr(workspace),
-                                       workspace.numel(), _stream(stream)), "ptl_kv_copy_pages")
+    with _On(kv.codes) as on:
+        _check(lib().ptl_kv_copy_pages(kv._ref, src.data_ptr(), dst.data_ptr(), src.numel(), workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), on.stream(stream)),
+               "ptl_kv_copy_pages")
     return kv
 
 
