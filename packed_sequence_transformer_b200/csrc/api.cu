@@ -817,7 +817,7 @@ ptl_status ptl_kv_append(const void* qkv, const int32_t* cu_seqlens, int32_t num
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int32_t* err = static_cast<int32_t*>(workspace);
   mark(st, PTL_KERNEL_CLEAR);
-  if (cudaMemsetAsync(err, 0, sizeof(int32_t), st) != cudaSuccess) return PTL_ERR_CUDA;
+  PTL_TRY(launch_kv_clear(err, sizeof(int32_t), st));
   EndMark end_mark{st};
   mark(st, PTL_KERNEL_KV_APPEND);
   const KvAppendArgs a{qkv, cu_seqlens, page_table, past_lens, kv->codes, kv->scales, err,
@@ -840,7 +840,7 @@ ptl_status ptl_kv_copy_pages(const ptl_kv_pages* kv, const int32_t* src, const i
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int32_t* err = static_cast<int32_t*>(workspace);
   mark(st, PTL_KERNEL_CLEAR);
-  if (cudaMemsetAsync(err, 0, sizeof(int32_t), st) != cudaSuccess) return PTL_ERR_CUDA;
+  PTL_TRY(launch_kv_clear(err, sizeof(int32_t), st));
   EndMark end_mark{st};
   mark(st, PTL_KERNEL_KV_COPY);
   PTL_TRY(launch_kv_copy(kv->codes, kv->scales, kv->num_pages, src, dst, count, err, st));
@@ -878,7 +878,7 @@ ptl_status ptl_attention_paged(const void* qkv, void* attn, const int32_t* cu_se
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
   mark(st, PTL_KERNEL_CLEAR);
-  if (cudaMemsetAsync(ws, 0, kPagedClear, st) != cudaSuccess) return PTL_ERR_CUDA;
+  PTL_TRY(launch_kv_clear(ws, kPagedClear, st));
   EndMark end_mark{st};
   mark(st, PTL_KERNEL_ATTENTION);
   const PagedArgs a{qkv, attn, cu_seqlens, page_table, past_lens, kv->codes, kv->scales,

@@ -142,7 +142,6 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
     for (int i = 0; i < PA_STAGES; ++i) mbar_init(&bar[i], 1);
     fence_mbar_init();
   }
-  pdl_wait();
   pdl_trigger();
 
   // every block counts the call's steps by itself: a sum per thread, a scan
@@ -162,6 +161,7 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
   }
   if (__syncthreads_or(bad)) {  // every block sees the same offsets: nothing is written
     const int offsets = __syncthreads_or(bad & 1);
+    pdl_wait();
     if (blockIdx.x == 0 && tid == 0) set_error(a.err, offsets ? PTL_ERR_BAD_OFFSETS : PTL_ERR_BAD_PAGE);
     return;
   }
@@ -188,8 +188,19 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
   // PA_PARTS (one block adds them up)
   int64_t G = W < int64_t(gridDim.x) ? W : int64_t(gridDim.x);
   if (longest > PA_PARTS && G * longest > PA_PARTS * W) G = PA_PARTS * W / longest;
-  if (int64_t(blockIdx.x) >= G) return;
-  const int64_t A = blockIdx.x * W / G, B = (blockIdx.x + 1) * W / G;
+  if (int64_t(blockIdx.x) >= G) {
+    pdl_wait();
+    return;
+  }
+  // (a 64-bit division costs a small call a noticeable part of its time)
+  int64_t A, B;
+  if (W < (1 << 22)) {
+    A = uint32_t(blockIdx.x * uint32_t(W)) / uint32_t(G);
+    B = uint32_t((blockIdx.x + 1) * uint32_t(W)) / uint32_t(G);
+  } else {
+    A = blockIdx.x * W / G;
+    B = (blockIdx.x + 1) * W / G;
+  }
   if (A >= base && A < base + mine) {
     int64_t left = A - base;
     for (int u = u_lo; u < u_hi; ++u) {
@@ -245,6 +256,7 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
       if (key) {
         id = id_next;
         if (id < 0 || id >= a.num_pages) {  // reported; page 0 stands in, the output is undefined
+          pdl_wait();
           set_error(a.err, PTL_ERR_BAD_PAGE);
           id = 0;
         }
@@ -507,6 +519,7 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
         }
         __threadfence();
         __syncwarp();
+        pdl_wait();  // the counters are zero
         int done = 0;
         if (lane == 0) done = atomicAdd(a.counters + c0 * H + head, 1);
         done = __shfl_sync(0xffffffffu, done, 0);
@@ -584,6 +597,7 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
     if (lane == 0 && i + 1 < steps) cw.next(a);
     __syncwarp();
   }
+  pdl_wait();
   if (!ok) {
     set_error(a.err, PTL_ERR_TIMEOUT);
     // this warp's own copies must not land after the block has left

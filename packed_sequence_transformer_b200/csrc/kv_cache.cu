@@ -12,6 +12,21 @@
 namespace ptl {
 using namespace sm100;
 
+// Zeroes `words` of a call's workspace: the error word and what else must start
+// at zero.  The call's kernel is launched as its dependent and starts at once;
+// this one has waited for everything before the call by then, so that kernel
+// needs to wait for these zeros only where it counts or reports (a memset in
+// its place cost 2 to 3 us of a call's time).
+__global__ void __launch_bounds__(256) kv_clear_kernel(uint32_t* ws, int words) {
+  pdl_wait();
+  pdl_trigger();
+  for (int i = threadIdx.x; i < words; i += 256) ws[i] = 0;
+}
+
+int launch_kv_clear(void* ws, size_t bytes, cudaStream_t st) {
+  return launch_k(kv_clear_kernel, dim3(1), dim3(256), 0, st, static_cast<uint32_t*>(ws), int(bytes / 4));
+}
+
 // ------------------------------------------------------------------ append
 // For the touched page of a user and one of its sides, with x the new tokens'
 // values and, in a page that keeps r > 0 earlier tokens, s_old its scale:
@@ -21,17 +36,19 @@ using namespace sm100;
 // unless it falls into e4m3's subnormals; with any other scale each raise
 // would round every kept code once more.
 //
-// A block of 512 threads takes one (page, side) at a time: warp (head, half)
-// holds 32 tokens of one head in registers (one read of the input), the two
-// halves of a head meet in shared memory for the maximum, and the codes leave
-// from the registers.  Values are turned to [dim][token] on the way out: a
+// A block of 256 threads takes one (page, side, four heads) at a time: warp
+// (head, half) holds 32 tokens of one head in registers (one read of the
+// input), the two halves of a head meet in shared memory for the maximum, and
+// the codes leave from the registers.  One barrier an item: the next item is
+// looked up while this one's loads are under way.  Values are turned to [dim][token] on the way out: a
 // lane holds 4 consecutive tokens of 8 dims, so a 32-bit word of 4 tokens is
 // built in registers, and the words of a warp are exchanged through a
 // swizzled 2 KB tile (granule ^ dim / 8: the 8 lanes that store one word of 8
 // different rows hit 8 different 16-byte bank groups).
 // Every block works the list of pages out of the offsets by itself (a sum per
 // thread and a scan), which costs it a microsecond and saves a launch.
-constexpr int KVA_THREADS = 512;
+constexpr int KVA_THREADS = 256;
+constexpr int KVA_HEADS = KVA_THREADS / 64;  // heads of an item
 
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
   uint32_t out = 0;
@@ -51,17 +68,16 @@ __device__ __forceinline__ uint32_t byte_range(int lo, int hi) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 2 : 1) kv_append_kernel(const KvAppendArgs a) {
+__global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 3 : 2) kv_append_kernel(const KvAppendArgs a) {
   constexpr int VEC = 16 / sizeof(T);   // elements of a 16-byte load
   constexpr int NLD = 8 / VEC;          // loads of a lane's 8 dims
   __shared__ int64_t s_scan[KVA_THREADS / 32];
-  __shared__ uint32_t s_amax[H][2];
-  __shared__ int s_item[4];
+  __shared__ uint32_t s_amax[2][KVA_HEADS][2];
+  __shared__ int s_item[2][4];
   __shared__ __align__(16) uint8_t s_turn[KVA_THREADS / 32][KV_TILE / 2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int head = warp >> 1, half = warp & 1;
+  const int half = warp & 1;
   const int c = lane & 7, j = lane >> 3;  // dims 8c .. 8c + 7, token group
-  pdl_wait();
   pdl_trigger();
 
   // this thread's users, their touched pages
@@ -77,6 +93,7 @@ __global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 2 : 1) kv_append
   }
   if (__syncthreads_or(bad)) {  // every block sees the same offsets: nothing is written
     const int offsets = __syncthreads_or(bad & 1);
+    pdl_wait();
     if (blockIdx.x == 0 && tid == 0) set_error(a.err, offsets ? PTL_ERR_BAD_OFFSETS : PTL_ERR_BAD_PAGE);
     return;
   }
@@ -95,9 +112,10 @@ __global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 2 : 1) kv_append
     total += s_scan[w];
   }
 
-  for (int64_t it = blockIdx.x; it < 2 * total; it += gridDim.x) {
-    const int64_t ord = it >> 1;
-    const int side = int(it & 1);
+  // items: page, side, heads in that order, the page's parts next to one another
+  constexpr int PARTS = 2 * H / KVA_HEADS;
+  auto locate = [&](int64_t item, int* out) {
+    const int64_t ord = item / PARTS;
     if (ord >= base && ord < base + mine) {  // one thread's users hold the page
       int64_t left = ord - base;
       for (int u = u_lo; u < u_hi; ++u) {
@@ -105,21 +123,30 @@ __global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 2 : 1) kv_append
         const int64_t cnt = n > 0 ? ((p + n - 1) >> 6) - (p >> 6) + 1 : 0;
         if (left < cnt) {
           const int pg = (p >> 6) + int(left);
-          const int r = left == 0 ? p & 63 : 0;                // tokens that the page keeps
-          const int t0 = left == 0 ? 0 : 64 * pg - p;          // first new token of the page
-          s_item[0] = a.table[int64_t(u) * a.max_pages + pg];
-          s_item[1] = r;
-          s_item[2] = min(64 - r, n - t0);
-          s_item[3] = c0 + t0;
+          const int r = left == 0 ? p & 63 : 0;        // tokens that the page keeps
+          const int t0 = left == 0 ? 0 : 64 * pg - p;  // first new token of the page
+          out[0] = a.table[int64_t(u) * a.max_pages + pg];
+          out[1] = r;
+          out[2] = min(64 - r, n - t0);
+          out[3] = c0 + t0;
           break;
         }
         left -= cnt;
       }
     }
-    __syncthreads();
-    const int page = s_item[0], r = s_item[1], m = s_item[2], row0 = s_item[3];
+  };
+  int cur = 0;
+  if (int64_t(blockIdx.x) < PARTS * total) locate(blockIdx.x, s_item[0]);
+  __syncthreads();
+  for (int64_t it = blockIdx.x; it < PARTS * total; it += gridDim.x, cur ^= 1) {
+    const int sub = int(it % PARTS), side = sub / (H / KVA_HEADS);
+    const int head = (sub % (H / KVA_HEADS)) * KVA_HEADS + (warp >> 1);
+    const int page = s_item[cur][0], r = s_item[cur][1], m = s_item[cur][2], row0 = s_item[cur][3];
     const bool ok = page >= 0 && page < a.num_pages;
-    if (!ok && tid == 0) set_error(a.err, PTL_ERR_BAD_PAGE);
+    if (!ok) {
+      pdl_wait();
+      if (tid == 0) set_error(a.err, PTL_ERR_BAD_PAGE);
+    }
 
     // 32 tokens (8 per lane: two groups of 4 consecutive ones) x 8 dims
     uint4 raw[8 * NLD];
@@ -133,6 +160,7 @@ __global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 2 : 1) kv_append
         raw[i * NLD + k] = has ? __ldcs(reinterpret_cast<const uint4*>(in + int64_t(row0 + t - r) * QKV_N + k * VEC))
                                : make_uint4(0, 0, 0, 0);
     }
+    if (it + gridDim.x < PARTS * total) locate(it + gridDim.x, s_item[cur ^ 1]);
     auto value = [&](int i, int e) -> float {  // dim 8c + e of the lane's token i
       const T* x = reinterpret_cast<const T*>(&raw[i * NLD]);
       return to_f32<T>(x[e]);
@@ -150,12 +178,12 @@ __global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 2 : 1) kv_append
       }
     mx = __reduce_max_sync(0xffffffffu, mx);
     odd = __any_sync(0xffffffffu, odd);
-    if (lane == 0) s_amax[head][half] = mx;
+    if (lane == 0) s_amax[cur][warp >> 1][half] = mx;
     float* sp = a.scales + (int64_t(ok ? page : 0) * 2 + side) * H + head;
     const float s_old = r > 0 ? *sp : 0.f;
     __syncthreads();
-    if (!ok) continue;  // (uniform) the next round's first barrier orders s_item
-    mx = max(s_amax[head][0], s_amax[head][1]);
+    if (!ok) continue;  // (uniform)
+    mx = max(s_amax[cur][warp >> 1][0], s_amax[cur][warp >> 1][1]);
     // smallest k with max |x| <= 448 * 2^k = 1.75 * 2^(k + 8)
     const int ke = max(int((mx + 0x1FFFFFu) >> 23) - 127 - 8, KV_MIN_EXP);
     const float s = fmaxf(s_old, __uint_as_float(uint32_t(ke + 127) << 23));
@@ -231,13 +259,14 @@ __global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 2 : 1) kv_append
       __syncwarp();  // the tile is read before the next page's words are stored
     }
   }
+  pdl_wait();
 }
 
 int launch_kv_append(const KvAppendArgs& a, ptl_dtype dt, cudaStream_t st) {
   // at most T / 64 + 2 pages per user with tokens are touched, two sides each
   const int64_t users = a.U < a.T ? a.U : a.T;
-  const int64_t items = 2 * (a.T / KV_PAGE + 2 * users);
-  const int64_t most = int64_t(num_sms()) * (dt == PTL_BF16 ? 2 : 1);
+  const int64_t items = 2 * H / KVA_HEADS * (a.T / KV_PAGE + 2 * users);
+  const int64_t most = int64_t(num_sms()) * (dt == PTL_BF16 ? 3 : 2);
   const dim3 grid(unsigned(items < most ? items : most));
   const int r = dt == PTL_BF16 ? launch_k(kv_append_kernel<__nv_bfloat16>, grid, dim3(KVA_THREADS), 0, st, a)
                                : launch_k(kv_append_kernel<float>, grid, dim3(KVA_THREADS), 0, st, a);
@@ -255,13 +284,13 @@ __global__ void __launch_bounds__(KVC_THREADS) kv_copy_kernel(uint8_t* codes, fl
                                                               const int32_t* __restrict__ src,
                                                               const int32_t* __restrict__ dst, int64_t n,
                                                               int32_t* err) {
-  pdl_wait();
   pdl_trigger();
   for (int64_t it = blockIdx.x; it < n * KVC_PARTS; it += gridDim.x) {
     const int64_t i = it / KVC_PARTS;
     const int part = int(it % KVC_PARTS);
     const int s = src[i], d = dst[i];
     if (s < 0 || s >= num_pages || d < 0 || d >= num_pages) {
+      pdl_wait();
       if (threadIdx.x == 0) set_error(err, PTL_ERR_BAD_PAGE);
       continue;
     }
@@ -274,6 +303,7 @@ __global__ void __launch_bounds__(KVC_THREADS) kv_copy_kernel(uint8_t* codes, fl
     for (int k = 0; k < 4; ++k) to[k * KVC_THREADS + threadIdx.x] = v[k];
     if (part == 0 && threadIdx.x < 2 * H) scales[int64_t(d) * 2 * H + threadIdx.x] = scales[int64_t(s) * 2 * H + threadIdx.x];
   }
+  pdl_wait();
 }
 
 int launch_kv_copy(uint8_t* codes, float* scales, int num_pages, const int32_t* src, const int32_t* dst, int64_t n,

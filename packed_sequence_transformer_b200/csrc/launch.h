@@ -176,7 +176,10 @@ int launch_gemm_moe2(const CUtensorMap& hbuf, const CUtensorMap& w2, const CUten
 int launch_gemm_fp8(const CUtensorMap& xq, const CUtensorMap& wq, const CUtensorMap& out_map, const float* sx,
                     const float* sw, const float* bias, int M, int N, int Kd, int32_t* err, cudaStream_t st);
 
-// kv_cache.cu: new tokens into the paged cache; page dst[i] = page src[i]
+// kv_cache.cu: zeroes the head of a workspace (the kernel launched next waits
+// for it before it counts or reports)
+int launch_kv_clear(void* ws, size_t bytes, cudaStream_t st);
+// new tokens into the paged cache; page dst[i] = page src[i]
 int launch_kv_append(const KvAppendArgs& a, ptl_dtype dt, cudaStream_t st);
 int launch_kv_copy(uint8_t* codes, float* scales, int num_pages, const int32_t* src, const int32_t* dst, int64_t n,
                    int32_t* err, cudaStream_t st);
