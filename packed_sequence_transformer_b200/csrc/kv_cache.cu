@@ -68,7 +68,7 @@ __device__ __forceinline__ uint32_t byte_range(int lo, int hi) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 3 : 2) kv_append_kernel(const KvAppendArgs a) {
+__global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 4 : 2) kv_append_kernel(const KvAppendArgs a) {
   constexpr int VEC = 16 / sizeof(T);   // elements of a 16-byte load
   constexpr int NLD = 8 / VEC;          // loads of a lane's 8 dims
   __shared__ int64_t s_scan[KVA_THREADS / 32];
@@ -161,23 +161,40 @@ __global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 3 : 2) kv_append
                                : make_uint4(0, 0, 0, 0);
     }
     if (it + gridDim.x < PARTS * total) locate(it + gridDim.x, s_item[cur ^ 1]);
-    auto value = [&](int i, int e) -> float {  // dim 8c + e of the lane's token i
-      const T* x = reinterpret_cast<const T*>(&raw[i * NLD]);
-      return to_f32<T>(x[e]);
-    };
-    // largest finite magnitude; NaN and infinities count as NaN
+    // largest finite magnitude; NaN and infinities count as NaN.  As integers
+    // magnitudes are ordered like the numbers; anything not finite is taken out
+    // in a second look that ordinary inputs never need.
     uint32_t mx = 0;
-    bool odd = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8 * NLD; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t b = __float_as_uint(value(i, e)) & 0x7FFFFFFFu;
-        odd |= b >= 0x7F800000u;
-        mx = max(mx, b >= 0x7F800000u ? 0u : b);
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(T) == 2)
+          mx = __vmaxu2(mx, w[k] & 0x7FFF7FFFu);
+        else
+          mx = max(mx, w[k] & 0x7FFFFFFFu);
       }
+    }
+    if constexpr (sizeof(T) == 2) mx = max(mx << 16, mx & 0xFFFF0000u);  // as fp32 bits
     mx = __reduce_max_sync(0xffffffffu, mx);
-    odd = __any_sync(0xffffffffu, odd);
+    const bool odd = mx >= 0x7F800000u;  // (of the warp)
+    if (odd) {
+      mx = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          uint32_t& word = reinterpret_cast<uint32_t*>(raw)[i * 4 * NLD + e * int(sizeof(T)) / 4];
+          const int sh = sizeof(T) == 2 ? 16 * (e & 1) : 0;
+          const uint32_t b = (sizeof(T) == 2 ? (word >> sh) << 16 : word) & 0x7FFFFFFFu;
+          if (b < 0x7F800000u)
+            mx = max(mx, b);
+          else
+            word |= sizeof(T) == 2 ? 0x7FFFu << sh : 0x7FFFFFFFu;  // a NaN
+        }
+      mx = __reduce_max_sync(0xffffffffu, mx);
+    }
     if (lane == 0) s_amax[cur][warp >> 1][half] = mx;
     float* sp = a.scales + (int64_t(ok ? page : 0) * 2 + side) * H + head;
     const float s_old = r > 0 ? *sp : 0.f;
@@ -190,11 +207,28 @@ __global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 3 : 2) kv_append
     const float inv = __fdiv_rn(1.0f, s), ratio = s_old * inv;
     const bool grow = r > 0 && s > s_old;
     if (half == 0 && lane == 0) *sp = s;
-    auto scaled = [&](int i, int e) -> float {
-      const float x = value(i, e);
-      if (odd && (__float_as_uint(x) & 0x7FFFFFFFu) >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
-      return x * inv;
+    // dims 8c + e and 8c + e + 1 (e even) of the lane's token i, over the scale
+    auto pair = [&](int i, int e) -> float2 {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(raw) + i * 4 * NLD + e * int(sizeof(T)) / 4;
+      float x, y;
+      if constexpr (sizeof(T) == 2) {
+        x = __uint_as_float(w[0] << 16);
+        y = __uint_as_float(w[0] & 0xFFFF0000u);
+      } else {
+        x = __uint_as_float(w[0]);
+        y = __uint_as_float(w[1]);
+      }
+      return make_float2(x * inv, y * inv);
     };
+    auto codes4 = [&](int i, int e) -> uint32_t {  // four dims of a token
+      const float2 p = pair(i, e), q = pair(i, e + 2);
+      return uint32_t(cvt_e4m3x2(p.x, p.y)) | uint32_t(cvt_e4m3x2(q.x, q.y)) << 16;
+    };
+    // a warp whose 32 tokens are all old or all absent has zeros to write or
+    // kept codes to rescale, but nothing to convert
+    const int t_lo = 32 * half;
+    const bool any = r < t_lo + 32 && r + m > t_lo;
+    if (!any && r > 0 && !(grow && t_lo < r)) continue;  // (the barrier above is an item's only one)
     uint8_t* tile = a.codes + int64_t(page) * KV_PAGE_BYTES + side * KV_SIDE + head * KV_TILE;
     if (side == 0) {
 #pragma unroll
@@ -202,10 +236,7 @@ __global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 3 : 2) kv_append
         const int t = 32 * half + 4 * (j + 4 * (i >> 2)) + (i & 3);
         uint2* dst = reinterpret_cast<uint2*>(tile + t * DH + 8 * c);
         if (t >= r && (t < r + m || r == 0)) {  // a page begun by this call is written whole, zeros behind the tokens
-          uint2 w;
-          w.x = uint32_t(cvt_e4m3x2(scaled(i, 0), scaled(i, 1))) | uint32_t(cvt_e4m3x2(scaled(i, 2), scaled(i, 3))) << 16;
-          w.y = uint32_t(cvt_e4m3x2(scaled(i, 4), scaled(i, 5))) | uint32_t(cvt_e4m3x2(scaled(i, 6), scaled(i, 7))) << 16;
-          *dst = w;
+          *dst = any ? make_uint2(codes4(i, 0), codes4(i, 4)) : make_uint2(0, 0);
         } else if (t < r && grow) {
           const uint2 w = *dst;
           *dst = make_uint2(rescale4(w.x, ratio), rescale4(w.y, ratio));
@@ -213,48 +244,50 @@ __global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 3 : 2) kv_append
       }
     } else {
       uint8_t* turn = s_turn[warp];
+      if (any) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int d = 8 * c + e;
-          const uint32_t w = uint32_t(cvt_e4m3x2(scaled(4 * q, e), scaled(4 * q + 1, e))) |
-                             uint32_t(cvt_e4m3x2(scaled(4 * q + 2, e), scaled(4 * q + 3, e))) << 16;
-          *reinterpret_cast<uint32_t*>(turn + 16 * ((2 * d + q) ^ c) + 4 * j) = w;
-        }
-      __syncwarp();
-      const int t_lo = 32 * half;
-      const bool touched = (r < t_lo + 32 && r + m > t_lo) || (grow && t_lo < r);
-      if (r == 0 || touched) {
+          for (int e = 0; e < 8; e += 2) {
+            const float2 t0 = pair(4 * q, e), t1 = pair(4 * q + 1, e);
+            const float2 t2 = pair(4 * q + 2, e), t3 = pair(4 * q + 3, e);
+            const int d = 8 * c + e;
+            *reinterpret_cast<uint32_t*>(turn + 16 * ((2 * d + q) ^ c) + 4 * j) =
+                uint32_t(cvt_e4m3x2(t0.x, t1.x)) | uint32_t(cvt_e4m3x2(t2.x, t3.x)) << 16;
+            *reinterpret_cast<uint32_t*>(turn + 16 * ((2 * d + 2 + q) ^ c) + 4 * j) =
+                uint32_t(cvt_e4m3x2(t0.y, t1.y)) | uint32_t(cvt_e4m3x2(t2.y, t3.y)) << 16;
+          }
+        __syncwarp();
+      }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int d = lane + 32 * k;
-          uint4 w[2];
-          uint4* dst = reinterpret_cast<uint4*>(tile + d * KV_PAGE + t_lo);
+      for (int k = 0; k < 2; ++k) {
+        const int d = lane + 32 * k;
+        uint4 w[2];
+        uint4* dst = reinterpret_cast<uint4*>(tile + d * KV_PAGE + t_lo);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) w[q] = *reinterpret_cast<const uint4*>(turn + 16 * ((2 * d + q) ^ (d >> 3)));
-          if (r > 0) {  // the row's other bytes stay (or are rescaled)
+        for (int q = 0; q < 2; ++q)
+          w[q] = any ? *reinterpret_cast<const uint4*>(turn + 16 * ((2 * d + q) ^ (d >> 3))) : make_uint4(0, 0, 0, 0);
+        if (r > 0) {  // the row's other bytes stay (or are rescaled)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint4 o = dst[q];
-              uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
-              uint32_t* nw = reinterpret_cast<uint32_t*>(&w[q]);
+          for (int q = 0; q < 2; ++q) {
+            uint4 o = dst[q];
+            uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
+            uint32_t* nw = reinterpret_cast<uint32_t*>(&w[q]);
 #pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                const int t = t_lo + 16 * q + 4 * b;
-                const uint32_t isnew = byte_range(r - t, r + m - t);
-                uint32_t keep = ow[b];
-                if (grow) {
-                  const uint32_t kept = byte_range(0, r - t);
-                  keep = (rescale4(keep, ratio) & kept) | (keep & ~kept);
-                }
-                nw[b] = (nw[b] & isnew) | (keep & ~isnew);
+            for (int b = 0; b < 4; ++b) {
+              const int t = t_lo + 16 * q + 4 * b;
+              const uint32_t isnew = byte_range(r - t, r + m - t);
+              uint32_t keep = ow[b];
+              if (grow) {
+                const uint32_t kept = byte_range(0, r - t);
+                keep = (rescale4(keep, ratio) & kept) | (keep & ~kept);
               }
+              nw[b] = (nw[b] & isnew) | (keep & ~isnew);
             }
           }
-          dst[0] = w[0];
-          dst[1] = w[1];
         }
+        dst[0] = w[0];
+        dst[1] = w[1];
       }
       __syncwarp();  // the tile is read before the next page's words are stored
     }
@@ -266,7 +299,7 @@ int launch_kv_append(const KvAppendArgs& a, ptl_dtype dt, cudaStream_t st) {
   // at most T / 64 + 2 pages per user with tokens are touched, two sides each
   const int64_t users = a.U < a.T ? a.U : a.T;
   const int64_t items = 2 * H / KVA_HEADS * (a.T / KV_PAGE + 2 * users);
-  const int64_t most = int64_t(num_sms()) * (dt == PTL_BF16 ? 3 : 2);
+  const int64_t most = int64_t(num_sms()) * (dt == PTL_BF16 ? 4 : 2);
   const dim3 grid(unsigned(items < most ? items : most));
   const int r = dt == PTL_BF16 ? launch_k(kv_append_kernel<__nv_bfloat16>, grid, dim3(KVA_THREADS), 0, st, a)
                                : launch_k(kv_append_kernel<float>, grid, dim3(KVA_THREADS), 0, st, a);
