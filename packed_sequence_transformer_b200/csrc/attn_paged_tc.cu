@@ -545,13 +545,19 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
           nan_any = __any_sync(0xffffffffu, nan_any);
         }
         const uint32_t dst = smem_u32(sKV + st * PTC_STAGE);
-#pragma unroll 4
-        for (int p = 0; p < 8; ++p) {  // keys, values
-          const uint4 v = *reinterpret_cast<const uint4*>(src + 1024 * p);
-          st_shared_v4(dst + 2048 * p + swz0, e4m3x2_to_half2(v.x), e4m3x2_to_half2(v.x >> 16), e4m3x2_to_half2(v.y),
-                       e4m3x2_to_half2(v.y >> 16));
-          st_shared_v4(dst + 2048 * p + swz1, e4m3x2_to_half2(v.z), e4m3x2_to_half2(v.z >> 16), e4m3x2_to_half2(v.w),
-                       e4m3x2_to_half2(v.w >> 16));
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // keys, values
+          uint4 v[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) v[p] = *reinterpret_cast<const uint4*>(src + half * KV_TILE + 1024 * p);
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const uint32_t to = dst + half * PTC_OPERAND + 2048 * p;
+            st_shared_v4(to + swz0, e4m3x2_to_half2(v[p].x), e4m3x2_to_half2(v[p].x >> 16), e4m3x2_to_half2(v[p].y),
+                         e4m3x2_to_half2(v[p].y >> 16));
+            st_shared_v4(to + swz1, e4m3x2_to_half2(v[p].z), e4m3x2_to_half2(v[p].z >> 16), e4m3x2_to_half2(v[p].w),
+                         e4m3x2_to_half2(v[p].w >> 16));
+          }
         }
         if (lane == 0) reinterpret_cast<uint32_t*>(&s_hasnan[st])[cw & 1] = nan_any;
         fence_proxy_async_smem();
