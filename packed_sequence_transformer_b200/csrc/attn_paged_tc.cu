@@ -140,10 +140,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 
 // One unit and the pages of it that this block has.  Costs, not pages, are
-// laid end to end: a page of a two-tile unit counts 2, one of a one-tile unit 1.
-// A page belongs to the block that its first cost falls into, and blocks have
-// at least two costs each, so every block between a unit's first and last has
-// a page of it.
+// laid end to end: a page of a two-tile unit counts 2, one of a one-tile unit 1
+// (measured 0.92 and 0.51 us), and a unit's first page PTC_UNIT more, what
+// beginning and ending a unit costs.  A page belongs to the block that its
+// first cost falls into, and blocks have at least PTC_UNIT + 2 costs each, so
+// every block between a unit's first and last has a page of it.
+constexpr int PTC_UNIT = 8;
 struct PagedTcUnit {
   int u, q0, head, n, past, k0, k1;
   bool two;
@@ -153,16 +155,23 @@ struct PagedTcUnit {
     n = a.cu[u + 1] - a.cu[u];
     past = a.past[u];
   }
-  __device__ __forceinline__ int64_t cost() const { return int64_t(span.count) << int(two); }
+  __device__ __forceinline__ int64_t cost() const { return PTC_UNIT + (int64_t(span.count) << int(two)); }
+  // where the last page's cost begins
+  __device__ __forceinline__ int64_t last_page() const { return span.count == 1 ? start : start + cost() - (1 << int(two)); }
   __device__ __forceinline__ void see(const PagedArgs& a, int64_t A, int64_t B) {
     two = n - q0 > 128;
     span = page_span(past + q0, past + min(q0 + PTC_QB, n) - 1, a.window, a.sinks);
     mine(A, B);
   }
+  // how many of the unit's pages begin before cost x
+  __device__ __forceinline__ int before(int64_t x) const {
+    if (x <= start) return 0;
+    const int64_t r = two ? 1 : 0, k = (x - start - PTC_UNIT + r) >> r;
+    return k < 1 ? 1 : k > span.count ? span.count : int(k);
+  }
   __device__ __forceinline__ void mine(int64_t A, int64_t B) {
-    const int64_t r = two ? 1 : 0;
-    k0 = A <= start ? 0 : int((A - start + r) >> r);
-    k1 = B >= start + cost() ? span.count : int((B - start + r) >> r);
+    k0 = before(A);
+    k1 = before(B);
   }
   // the next unit; false when it starts at or behind B
   __device__ __forceinline__ bool next(const PagedArgs& a, int64_t A, int64_t B) {
@@ -237,8 +246,8 @@ __device__ __forceinline__ int64_t paged_tc_user_cost(const PagedArgs& a, int n,
   int64_t s = 0;
   if (n > a.few)
     for (int q0 = 0; q0 < n; q0 += PTC_QB)
-      s += int64_t(H * page_span(past + q0, past + min(q0 + PTC_QB, n) - 1, a.window, a.sinks).count)
-           << (n - q0 > 128 ? 1 : 0);
+      s += H * (PTC_UNIT + (int64_t(page_span(past + q0, past + min(q0 + PTC_QB, n) - 1, a.window, a.sinks).count)
+                            << (n - q0 > 128 ? 1 : 0)));
   return s;
 }
 
@@ -261,7 +270,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
   __shared__ float s_c[2][PTC_QB];                         // [slot][row] exponent's factor
   __shared__ float s_xm[PTC_GROUPS][128], s_xl[PTC_GROUPS][128];  // maxima and sums handed over
   __shared__ uint64_t s_xnan[PTC_GROUPS][128];
-  __shared__ float s_w[PTC_GROUPS][128];                   // weights of a part being added
+  __shared__ float s_wm[PTC_GROUPS][128], s_wl[PTC_GROUPS][128];  // of the rows whose parts are added
   __shared__ int64_t s_scan[PTC_THREADS / 32];
   __shared__ int64_t s_start;
   __shared__ int s_first[3];
@@ -295,7 +304,6 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
     }
     fence_mbar_init();
   }
-  pdl_wait();
   pdl_trigger();
 
   // the call's costs, counted by every block (see attn_paged.cu)
@@ -310,7 +318,10 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
     else
       mine += paged_tc_user_cost(a, n, p);
   }
-  if (__syncthreads_or(bad)) return;  // attn_paged_kernel reports it
+  if (__syncthreads_or(bad)) {  // attn_paged_kernel reports it
+    pdl_wait();
+    return;
+  }
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -325,8 +336,11 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
     if (w < warp) base += s_scan[w];
     W += s_scan[w];
   }
-  const int64_t G = min(int64_t(gridDim.x), W >> 1 > 0 ? W >> 1 : W);
-  if (int64_t(blockIdx.x) >= G) return;
+  const int64_t G = min(int64_t(gridDim.x), max(W / (PTC_UNIT + 2), min(W, int64_t(1))));
+  if (int64_t(blockIdx.x) >= G) {
+    pdl_wait();
+    return;
+  }
   const int64_t A = blockIdx.x * W / G, B = (blockIdx.x + 1) * W / G;
   if (A >= base && A < base + mine) {
     int64_t left = A - base;
@@ -338,8 +352,8 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
         continue;
       }
       for (int q0 = 0; q0 < n; q0 += PTC_QB) {
-        const int64_t c = int64_t(page_span(p + q0, p + min(q0 + PTC_QB, n) - 1, a.window, a.sinks).count)
-                          << (n - q0 > 128 ? 1 : 0);
+        const int64_t c = PTC_UNIT + (int64_t(page_span(p + q0, p + min(q0 + PTC_QB, n) - 1, a.window, a.sinks).count)
+                                      << (n - q0 > 128 ? 1 : 0));
         if (left < H * c) {
           s_first[0] = u;
           s_first[1] = q0;
@@ -406,7 +420,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
         p.first = w.span.first;
         // block k starts at cost k W / G
         p.c0 = int(((w.start + 1) * G - 1) / W);
-        p.c1 = int(((w.start + w.cost() - (w.two ? 2 : 1) + 1) * G - 1) / W);
+        p.c1 = int(((w.last_page() + 1) * G - 1) / W);
         p.tile[0].set(a, w, 0);
         p.tile[1].set(a, w, w.two ? 1 : 0);
       }
@@ -441,6 +455,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
       if (more) {
         int id = id_next;
         if (id < 0 || id >= a.num_pages) {  // reported; page 0 stands in, the output is undefined
+          pdl_wait();
           if (lane == 0) set_error(a.err, PTL_ERR_BAD_PAGE);
           id = 0;
         }
@@ -840,6 +855,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
         nans |= s_xnan[g + d][r];
       }
       m = M;
+      if (c0 != c1) pdl_wait();  // the counters are zero, the parts' room is free
       auto part = [&](int i) { return a.partial + (int64_t(2 * i + (i == c0 ? 1 : 0)) * 2 + tile) * PTC_PART; };
       float* mp = part(blockIdx.x);
       const float inv = 1.0f / l;
@@ -893,8 +909,8 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
       if (r == 0) s_done[g] = atomicAdd(a.counters + PAGED_MAX_CTAS * H + 2 * c0 + tile, 1);
       if (!meet()) break;
       if (s_done[g] != c1 - c0) continue;
-      // the last part: add them up, in block order.  Thread r weighs row r, then
-      // holds 4 dims of each 8th row; a part's loads are in flight together.
+      // The last part: add them up, in block order.  Thread r finds row r's
+      // maximum and sum, then holds 4 dims of each 8th row.
       __threadfence();
       M = -INFINITY;
       float L = 0.f;
@@ -908,40 +924,43 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
           L = fmaf(ex2_approx(ml.x - M), ml.y, L);
         }
       }
+      s_wm[g][r] = M;
+      s_wl[g][r] = 1.0f / L;
+      if (!meet()) break;
 #pragma unroll 1
       for (int h = 0; h < 4; ++h) {  // 32 rows at a time
+        const int first = 32 * h + (r >> 4);
         float4 acc[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int row0 = 32 * h + (r >> 4);
+#pragma unroll 2
         for (int i = c0; i <= c1; ++i) {
-          const float* mp2 = part(i);
-          s_w[g][r] = r < rows ? ex2_approx(__ldcg(mp2 + 128 * DH + 2 * r) - M) / L : 0.f;
-          if (!meet()) break;
-          float4 v[4];
+          const float* pi = part(i);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (row0 + 8 * j < rows) v[j] = __ldcg(reinterpret_cast<const float4*>(mp2 + (row0 + 8 * j) * DH) + (r & 15));
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (row0 + 8 * j < rows) {
-              const float we = s_w[g][row0 + 8 * j];
-              acc[j].x = fmaf(we, v[j].x, acc[j].x);
-              acc[j].y = fmaf(we, v[j].y, acc[j].y);
-              acc[j].z = fmaf(we, v[j].z, acc[j].z);
-              acc[j].w = fmaf(we, v[j].w, acc[j].w);
-            }
-          if (!meet()) break;
+          for (int j = 0; j < 4; ++j) {
+            const int row = first + 8 * j;
+            if (row >= rows) continue;
+            const float we = ex2_approx(__ldcg(pi + 128 * DH + 2 * row) - s_wm[g][row]);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(pi + row * DH) + (r & 15));
+            acc[j].x = fmaf(we, v.x, acc[j].x);
+            acc[j].y = fmaf(we, v.y, acc[j].y);
+            acc[j].z = fmaf(we, v.z, acc[j].z);
+            acc[j].w = fmaf(we, v.w, acc[j].w);
+          }
         }
-        if (!ok) break;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (row0 + 8 * j < rows)
-            *reinterpret_cast<uint2*>(out + int64_t(row0 + 8 * j) * D + 4 * (r & 15)) =
-                make_uint2(pack_bf16x2(acc[j].x, acc[j].y), pack_bf16x2(acc[j].z, acc[j].w));
+        for (int j = 0; j < 4; ++j) {
+          const int row = first + 8 * j;
+          if (row >= rows) continue;
+          const float iv = s_wl[g][row];
+          *reinterpret_cast<uint2*>(out + int64_t(row) * D + 4 * (r & 15)) =
+              make_uint2(pack_bf16x2(acc[j].x * iv, acc[j].y * iv), pack_bf16x2(acc[j].z * iv, acc[j].w * iv));
+        }
       }
+      if (!meet()) break;  // before another unit's rows take the places of these
     }
   }
+  pdl_wait();
   if (!ok) set_error(a.err, PTL_ERR_TIMEOUT);
   __syncwarp();
   tc_fence_before();
