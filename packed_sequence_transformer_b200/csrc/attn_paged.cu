@@ -7,7 +7,7 @@
 // block, so that one long history is spread over all SMs and many short ones
 // share them evenly.  A block has one warp per head; the warps never meet.
 // A warp streams its head's 4 KB key and value tiles through a ring of its own
-// (plain bulk copies, KVR_STAGES deep, about 190 KB in flight per SM) and
+// (plain bulk copies, about 190 KB in flight per SM) and
 // computes, per page, on the tensor cores:
 //   S[token][query] = K Q^T, 64 x 8, codes converted to fp16 (exact) straight
 //     from 16-byte reads of the tile: a lane's 16 bytes are 16 consecutive
@@ -44,8 +44,14 @@ using namespace sm100;
 constexpr int PA_THREADS = 32 * H;
 constexpr int PA_QG = 8;        // queries of a unit
 constexpr int PA_PARTS = 128;   // blocks that share a unit, at most about
-constexpr int PA_STAGES = 3;    // 4 KB tiles in a warp's ring
-constexpr int PA_SMEM = H * PA_STAGES * KV_TILE;
+// 4 KB tiles in a warp's ring, about 190 KB an SM: two blocks of the bf16 build,
+// one of the fp32 build, whose two-part operands need the registers of both
+// (with two blocks it spilled: 36 us instead of 26 for 5 new tokens of 60 users
+// over 700).
+template <int SPLIT>
+constexpr int PA_STAGES = SPLIT == 1 ? 3 : 6;
+template <int SPLIT>
+constexpr int PA_BLOCKS = SPLIT == 1 ? 2 : 1;
 constexpr int PA_PART = PA_QG * (DH + 2);  // floats of one head's part: O, then (m, l) per query
 
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -126,9 +132,10 @@ __device__ __forceinline__ int64_t paged_user_steps(const PagedArgs& a, int n, i
 }
 
 template <typename T, int SPLIT>
-__global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS<SPLIT>) attn_paged_kernel(const PagedArgs a) {
+  constexpr int STAGES = PA_STAGES<SPLIT>;
   extern __shared__ __align__(128) uint8_t ring_all[];
-  __shared__ uint64_t s_bar[H][PA_STAGES];
+  __shared__ uint64_t s_bar[H][STAGES];
   __shared__ int64_t s_scan[H];
   __shared__ int s_longest[H];
   __shared__ int s_first[3];
@@ -137,9 +144,9 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int head = warp, g = lane >> 2, t = lane & 3;
   uint64_t* bar = s_bar[warp];
-  uint8_t* ring = ring_all + warp * PA_STAGES * KV_TILE;
+  uint8_t* ring = ring_all + warp * STAGES * KV_TILE;
   if (lane == 0) {
-    for (int i = 0; i < PA_STAGES; ++i) mbar_init(&bar[i], 1);
+    for (int i = 0; i < STAGES; ++i) mbar_init(&bar[i], 1);
     fence_mbar_init();
   }
   pdl_trigger();
@@ -248,39 +255,42 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
   int64_t sent = 0, used = 0;
   int st_i = 0, st_c = 0, ph_c = 0;
   int id = 0, id_next = lane == 0 ? iw.entry(a) : 0;
-  float ks0 = 0.f, ks1 = 0.f, vs0 = 0.f, vs1 = 0.f;  // lane 0: scales of the pages under way, by parity
+  // Scales of the pages under way, the current one's among them at most 4 (a
+  // ring of 2 n tiles is at most n pages ahead): page i's in lane i % 4.
+  static_assert(STAGES / 2 + 1 <= 4, "lanes for the scales");
+  float ks_ahead = 0.f, vs_ahead = 0.f;
   auto issue = [&]() {
     if (sent >= 2 * steps) return;
-    if (lane == 0) {
-      const bool key = (sent & 1) == 0;
-      if (key) {
+    const bool key = (sent & 1) == 0;
+    if (key) {
+      if (lane == 0) {
         id = id_next;
         if (id < 0 || id >= a.num_pages) {  // reported; page 0 stands in, the output is undefined
           pdl_wait();
           set_error(a.err, PTL_ERR_BAD_PAGE);
           id = 0;
         }
-        const float* sc = a.scales + int64_t(id) * 2 * H + head;
-        if ((sent >> 1) & 1) {
-          ks1 = __ldg(sc);
-          vs1 = __ldg(sc + H);
-        } else {
-          ks0 = __ldg(sc);
-          vs0 = __ldg(sc + H);
-        }
         if ((sent >> 1) + 1 < steps) {
           iw.next(a);
           id_next = iw.entry(a);
         }
       }
+      const int page = __shfl_sync(0xffffffffu, id, 0);
+      if (lane == int((sent >> 1) & 3)) {
+        const float* sc = a.scales + int64_t(page) * 2 * H + head;
+        ks_ahead = __ldg(sc);
+        vs_ahead = __ldg(sc + H);
+      }
+    }
+    if (lane == 0) {
       mbar_arrive_expect_tx(&bar[st_i], KV_TILE);
       bulk_load(ring + st_i * KV_TILE, a.codes + int64_t(id) * KV_PAGE_BYTES + (key ? 0 : KV_SIDE) + head * KV_TILE,
                 KV_TILE, &bar[st_i]);
     }
     ++sent;
-    if (++st_i == PA_STAGES) st_i = 0;
+    if (++st_i == STAGES) st_i = 0;
   };
-  for (int i = 0; i < PA_STAGES; ++i) issue();
+  for (int i = 0; i < STAGES; ++i) issue();
 
   uint32_t qf[SPLIT][4][2];
   float cf[2];  // factor of this lane's two queries: softmax scale, log2 e, the row's power of two
@@ -329,8 +339,8 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
     }
-    const float ks = __shfl_sync(0xffffffffu, (i & 1) ? ks1 : ks0, 0);
-    const float vs = __shfl_sync(0xffffffffu, (i & 1) ? vs1 : vs0, 0);
+    const float ks = __shfl_sync(0xffffffffu, ks_ahead, int(i & 3));
+    const float vs = __shfl_sync(0xffffffffu, vs_ahead, int(i & 3));
 
     // S = K Q^T: row r of tile mt is token 16 (r / 2 % 4) + 4 mt + 2 (r / 8) + r % 2
     if (!mbar_wait(&bar[st_c], ph_c)) {
@@ -359,7 +369,7 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
     ++used;
     __syncwarp();  // the tile is read: its stage takes the next one
     issue();
-    if (++st_c == PA_STAGES) {
+    if (++st_c == STAGES) {
       st_c = 0;
       ph_c ^= 1;
     }
@@ -475,7 +485,7 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
     ++used;
     __syncwarp();
     issue();
-    if (++st_c == PA_STAGES) {
+    if (++st_c == STAGES) {
       st_c = 0;
       ph_c ^= 1;
     }
@@ -603,7 +613,7 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
     // this warp's own copies must not land after the block has left
     for (; used < sent; ++used) {
       mbar_wait(&bar[st_c], ph_c);
-      if (++st_c == PA_STAGES) {
+      if (++st_c == STAGES) {
         st_c = 0;
         ph_c ^= 1;
       }
@@ -611,22 +621,24 @@ __global__ void __launch_bounds__(PA_THREADS, 2) attn_paged_kernel(const PagedAr
   }
 }
 
-int paged_grid() {
-  const int g = 2 * num_sms();
+template <int SPLIT>
+static int paged_grid() {
+  const int g = PA_BLOCKS<SPLIT> * num_sms();
   return g < PAGED_MAX_CTAS ? g : PAGED_MAX_CTAS;
 }
 
 template <typename T, int SPLIT>
 static int launch_paged_t(const PagedArgs& a, cudaStream_t st) {
+  constexpr int smem = H * PA_STAGES<SPLIT> * KV_TILE;
   static PerDevice configured;
   if (configured.get([] {
         return cudaFuncSetAttribute(attn_paged_kernel<T, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    PA_SMEM) == cudaSuccess
+                                    smem) == cudaSuccess
                    ? 1
                    : -1;
       }) < 0)
     return -1;
-  if (launch_k(attn_paged_kernel<T, SPLIT>, dim3(paged_grid()), dim3(PA_THREADS), PA_SMEM, st, a) != 0) return -1;
+  if (launch_k(attn_paged_kernel<T, SPLIT>, dim3(paged_grid<SPLIT>()), dim3(PA_THREADS), smem, st, a) != 0) return -1;
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 

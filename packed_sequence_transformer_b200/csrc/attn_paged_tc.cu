@@ -145,7 +145,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // beginning and ending a unit costs.  A page belongs to the block that its
 // first cost falls into, and blocks have at least PTC_UNIT + 2 costs each, so
 // every block between a unit's first and last has a page of it.
-constexpr int PTC_UNIT = 8;
+constexpr int PTC_UNIT = 12;
 struct PagedTcUnit {
   int u, q0, head, n, past, k0, k1;
   bool two;

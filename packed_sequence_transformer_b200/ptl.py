@@ -231,8 +231,8 @@ class _On:
     made only where they are needed."""
     __slots__ = ("index", "guard")
 
-    def __init__(self, t: torch.Tensor):
-        self.index = t.device.index if t.is_cuda else -1
+    def __init__(self, index: int):
+        self.index = index
         self.guard = None
 
     def __enter__(self):
@@ -483,6 +483,7 @@ class KvPages:
         self.codes, self.scales = codes, scales
         self._struct = KvPagesStruct(_ptr(codes), _ptr(scales), n)
         self._ref = ctypes.byref(self._struct)
+        self.index = codes.get_device()  # -1: CPU tensors, which the library refuses
 
 
 def alloc_kv_pages(num_pages: int, device="cuda") -> KvPages:
@@ -491,7 +492,7 @@ def alloc_kv_pages(num_pages: int, device="cuda") -> KvPages:
                    torch.ones(num_pages, 2, 8, dtype=torch.float32, device=device))
 
 
-_I32, _U8 = torch.int32, torch.uint8
+_I32 = torch.int32
 
 
 def _check_paged(qkv, cu_seqlens, kv: KvPages, page_table, past_lens, workspace, attn=None):
@@ -499,7 +500,6 @@ def _check_paged(qkv, cu_seqlens, kv: KvPages, page_table, past_lens, workspace,
     users and table width."""
     T, width = qkv.shape
     users, max_pages = page_table.shape
-    dev = qkv.device
     if width != 1536:
         raise ValueError("qkv must be [T, 1536]")
     if past_lens.shape != (users,) or cu_seqlens.shape != (users + 1,):
@@ -508,14 +508,13 @@ def _check_paged(qkv, cu_seqlens, kv: KvPages, page_table, past_lens, workspace,
         raise ValueError("cu_seqlens, page_table and past_lens must be int32")
     if attn is not None and (attn.shape != (T, 512) or attn.dtype is not qkv.dtype):
         raise ValueError("attn must be [T, 512] of qkv's dtype")
+    index = kv.index
     for t in (qkv, cu_seqlens, page_table, past_lens, workspace) if attn is None else (
             qkv, cu_seqlens, page_table, past_lens, workspace, attn):
         if not t.is_contiguous():
             raise ValueError("tensors passed to libptl must be contiguous")
-        if t.device != dev:
+        if t.get_device() != index:  # (-1: a CPU tensor)
             raise ValueError("all tensors of a call must be on one device")
-    if kv.codes.device != dev:
-        raise ValueError("all tensors of a call must be on one device")
     return T, users, max_pages
 
 
@@ -523,7 +522,7 @@ def kv_append(qkv, cu_seqlens, kv: KvPages, page_table, past_lens, workspace, st
     """ptl_kv_append: the keys and values of qkv [T, 1536] into the pages, token
     i of user u at position past_lens[u] + i.  workspace: >= 256 bytes."""
     T, U, max_pages = _check_paged(qkv, cu_seqlens, kv, page_table, past_lens, workspace)
-    with _On(qkv) as on:
+    with _On(kv.index) as on:
         _check(lib().ptl_kv_append(qkv.data_ptr(), cu_seqlens.data_ptr(), U, T, _dt(qkv.dtype), kv._ref,
                                    page_table.data_ptr(), max_pages, past_lens.data_ptr(), workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), on.stream(stream)), "ptl_kv_append")
@@ -543,7 +542,7 @@ def attention_paged(qkv, attn, cu_seqlens, kv: KvPages, page_table, past_lens, w
     hold the new tokens too), causal, with window > 0 only the last `window`
     keys and the sequence's first `sinks`, into attn [T, 512]."""
     T, U, max_pages = _check_paged(qkv, cu_seqlens, kv, page_table, past_lens, workspace, attn)
-    with _On(qkv) as on:
+    with _On(kv.index) as on:
         _check(lib().ptl_attention_paged(qkv.data_ptr(), attn.data_ptr(), cu_seqlens.data_ptr(), U, T, _dt(qkv.dtype),
                                          kv._ref, page_table.data_ptr(), max_pages, past_lens.data_ptr(), window,
                                          sinks, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
@@ -558,9 +557,9 @@ def kv_copy_pages(kv: KvPages, src, dst, workspace, stream=None):
         raise ValueError("src and dst must be int32 lists of one length")
     if not (src.is_contiguous() and dst.is_contiguous() and workspace.is_contiguous()):
         raise ValueError("tensors passed to libptl must be contiguous")
-    if any(t.device != kv.codes.device for t in (src, dst, workspace)):
+    if any(t.get_device() != kv.index for t in (src, dst, workspace)):
         raise ValueError("all tensors of a call must be on one device")
-    with _On(kv.codes) as on:
+    with _On(kv.index) as on:
         _check(lib().ptl_kv_copy_pages(kv._ref, src.data_ptr(), dst.data_ptr(), src.numel(), workspace.data_ptr(),
                                        workspace.numel() * workspace.element_size(), on.stream(stream)),
                "ptl_kv_copy_pages")
