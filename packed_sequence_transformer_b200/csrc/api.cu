@@ -816,8 +816,6 @@ ptl_status ptl_kv_append(const void* qkv, const int32_t* cu_seqlens, int32_t num
   if ((s = device_ok()) != PTL_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int32_t* err = static_cast<int32_t*>(workspace);
-  mark(st, PTL_KERNEL_CLEAR);
-  PTL_TRY(launch_kv_clear(err, sizeof(int32_t), st));
   EndMark end_mark{st};
   mark(st, PTL_KERNEL_KV_APPEND);
   const KvAppendArgs a{qkv, cu_seqlens, page_table, past_lens, kv->codes, kv->scales, err,
@@ -839,8 +837,6 @@ ptl_status ptl_kv_copy_pages(const ptl_kv_pages* kv, const int32_t* src, const i
   if ((s = device_ok()) != PTL_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int32_t* err = static_cast<int32_t*>(workspace);
-  mark(st, PTL_KERNEL_CLEAR);
-  PTL_TRY(launch_kv_clear(err, sizeof(int32_t), st));
   EndMark end_mark{st};
   mark(st, PTL_KERNEL_KV_COPY);
   PTL_TRY(launch_kv_copy(kv->codes, kv->scales, kv->num_pages, src, dst, count, err, st));
