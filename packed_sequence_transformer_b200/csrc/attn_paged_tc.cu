@@ -224,7 +224,8 @@ struct PagedTcTile {
 // two-tile unit every second, in a one-tile unit every fourth.
 struct PagedTcShare {
   int turn, turns;
-  __device__ __forceinline__ PagedTcShare(bool two, int g) : turn(two ? g & 1 : g), turns(two ? 1 : 3) {}
+  // (a tile's first group, which also adds the sums up, comes last)
+  __device__ __forceinline__ PagedTcShare(bool two, int g) : turn((g + (two ? 1 : 3)) & (two ? 1 : 3)), turns(two ? 1 : 3) {}
   __device__ __forceinline__ int below(int x) const { return (x + turns - turn) >> (turns == 1 ? 1 : 2); }  // j < x
   __device__ __forceinline__ int pages(const PagedTcTile& t) const {
     return below(t.sink_end) + max(0, below(t.hi) - below(t.lo));
