@@ -13,7 +13,7 @@
 //     from 16-byte reads of the tile: a lane's 16 bytes are 16 consecutive
 //     dims, taken as the k positions of four m16n8k16 steps (the order of a
 //     contraction is free, Q is laid out to match);
-//   p = 2^(S - m) with the running maximum m of each query;
+//   p = 2^(S - m + 15) with the running maximum m of each query;
 //   O[dim][query] += V P, where P reaches the operand layout by one 8 x 8
 //     transposition per 8 tokens; tokens are dealt to the rows of S in the
 //     order in which the value tile's 16-byte reads deliver them.
@@ -48,6 +48,9 @@ constexpr int PA_PARTS = 128;   // blocks that share a unit, at most about
 // one of the fp32 build, whose two-part operands need the registers of both
 // (with two blocks it spilled: 36 us instead of 26 for 5 new tokens of 60 users
 // over 700).
+// The largest weight of a query is 2^PA_TOP, so that fp16 holds weights down to
+// 2^-39 of it (with 1 for the largest, all below 2^-25 were lost, however many).
+constexpr float PA_TOP = 15.f, PA_DOWN = 1.f / 32768.f;
 template <int SPLIT>
 constexpr int PA_STAGES = SPLIT == 1 ? 3 : 6;
 template <int SPLIT>
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS<SPLIT>) attn_paged_kerne
         for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
     }
     const float ks = __shfl_sync(0xffffffffu, ks_ahead, int(i & 3));
-    const float vs = __shfl_sync(0xffffffffu, vs_ahead, int(i & 3));
+    const float vs = __shfl_sync(0xffffffffu, vs_ahead, int(i & 3)) * PA_DOWN;
 
     // S = K Q^T: row r of tile mt is token 16 (r / 2 % 4) + 4 mt + 2 (r / 8) + r % 2
     if (!mbar_wait(&bar[st_c], ph_c)) {
@@ -412,8 +415,8 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS<SPLIT>) attn_paged_kerne
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
       const float mn = fmaxf(m[q], mx);
-      mu[q] = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every p is 2^-inf = 0
-      alpha[q] = ex2_approx(m[q] - mu[q]);
+      alpha[q] = mn == -INFINITY ? 0.f : ex2_approx(m[q] - mn);
+      mu[q] = mn == -INFINITY ? 0.f : mn - PA_TOP;  // nothing seen yet: every p is 2^-inf = 0
       m[q] = mn;
       l[q] *= alpha[q];
     }
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS<SPLIT>) attn_paged_kerne
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           if (2 * t + q >= nq) continue;
-          const float inv = 1.0f / l[q];
+          const float inv = 1.0f / (l[q] * PA_DOWN);
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
             dst[(2 * t + q) * D + 16 * d + g] = from_f32<T>(o[d][q] * inv);
@@ -555,7 +558,7 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS<SPLIT>) attn_paged_kerne
             M = mn;
           }
           if (M == -INFINITY) M = 0.f;
-          const float inv = 1.0f / L;
+          const float inv = 1.0f / (L * PA_DOWN);
           // 16 lanes hold a row, the two halves of the warp take parts in turn
           const int half = lane >> 4, d4 = lane & 15;
           auto add_up = [&](auto rows, auto depth, int q0) {

@@ -32,10 +32,12 @@
 //
 // Exponent: t = s q_row k_page + log2(v_page), w = 2^(t - m): the value scale,
 // a power of two, rides in the exponent, so that O accumulates over pages in
-// TMEM; the normaliser adds w / v_page.  The weights are computed with
-// the maximum of the pages before; only when a page exceeds that by 2^8 (fp16
-// would run out above) is m raised, O rescaled in place and the page computed
-// again.
+// TMEM; the normaliser adds w / v_page.  m comes from the maximum of the pages
+// before; only when a page exceeds that by 2^4 is m raised and O rescaled in
+// place.  A page of small values (v_page far below the others') may weigh
+// nothing in O and all in the normaliser: where its w would fall below what fp32
+// holds, they are taken relative to the page's own maximum and the normaliser's
+// part is scaled instead; factors of a normaliser are applied in two halves.
 // Values that are NaN codes in a page that some query does not see wholly are
 // taken out by the converters and given back, per row, to the queries that see
 // them.  Every wait is bounded.
@@ -73,7 +75,11 @@ constexpr int PTC_QTILE = 128 * 128;
 constexpr int PTC_RAW_BYTES = 2 * KV_TILE;
 constexpr int PTC_SMEM = 4 * PTC_QTILE + PTC_STAGES * PTC_STAGE + 2 * PTC_RAW * PTC_RAW_BYTES + 1024;
 constexpr int PTC_PART = 128 * (DH + 2);  // floats of one tile's part
-constexpr float PTC_RAISE = 8.f;
+// A tile's reference m lies 2^PTC_TOP below the largest exponent it was taken
+// from, and is taken anew when a page exceeds that by 2^PTC_RAISE: weights reach
+// 2^15 at most, and fp16 holds them to 2^-35 of the largest (with weights of 1
+// for the largest, what lay 2^-25 below it was lost, as much as 2^20 tokens of it).
+constexpr float PTC_TOP = 11.f, PTC_RAISE = 4.f;
 
 __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
@@ -133,6 +139,11 @@ __device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     if ((i & 63) == 0 && __any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs)) return false;
   }
+}
+// l 2^d, where 2^d alone may be below the smallest number
+__device__ __forceinline__ float scale_sum(float l, float d) {
+  const float e = ex2_approx(0.5f * d);
+  return l * e * e;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -747,11 +758,11 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
         }
         const float top = fmaf(fmaxf(mx[0], mx[1]), ck, mt.y);
         if (i == 0) {
-          m = top;
-        } else if (__any_sync(0xffffffffu, top > m + PTC_RAISE)) {
+          m = top - PTC_TOP;
+        } else if (__any_sync(0xffffffffu, top > m + (PTC_TOP + PTC_RAISE))) {
           // (the scores' arrival says that the products before are done)
-          const float mn = fmaxf(m, top);
-          const float alpha = mn == -INFINITY ? 1.f : ex2_approx(m - mn);
+          const float mn = fmaxf(m, top - PTC_TOP), d = mn == -INFINITY ? 0.f : m - mn;
+          const float alpha = ex2_approx(d);
 #pragma unroll 1
           for (int h = 0; h < 4; ++h) {
             uint32_t o[16];
@@ -760,10 +771,14 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
             tmem_st16(tO + 16 * h, o);
           }
-          l *= alpha;
+          l = scale_sum(l, d);
           m = mn;
         }
-        const float off = mt.y - (m == -INFINITY ? 0.f : m);
+        float off = mt.y - (m == -INFINITY ? 0.f : m), part = mt.z;
+        if (top < m - 64.f && top != -INFINITY) {  // nothing in O: weights of 2^-26 and less, which are 0 in fp16
+          off = mt.y - top - 26.f;
+          part = ex2_approx(top - m + 26.f - mt.y);
+        }
         const uint64_t ck2 = f2_pack(ck, ck), off2 = f2_pack(off, off);
         uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll 1
@@ -793,7 +808,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
         float a0, a1, a2, a3;
         f2_unpack(sum[0], a0, a1);
         f2_unpack(sum[1], a2, a3);
-        l = fmaf((a0 + a1) + (a2 + a3), mt.z, l);
+        l = fmaf((a0 + a1) + (a2 + a3), part, l);
         const uint2 has = s_hasnan[st];
         if (has.x | has.y) {
 #pragma unroll 1
@@ -847,12 +862,12 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
       // each group's weight takes the place of its maximum
       s_xm[g][r] = pages > 0 && M != -INFINITY ? ex2_approx(m - M) : 0.f;
       s_xl[g][r] = pages > 0 ? l : -1.f;
-      l *= s_xm[g][r];
+      l = M == -INFINITY ? 0.f : scale_sum(l, m - M);
 #pragma unroll 1
       for (int d = 1; d <= donors; ++d) {
-        const float ld = s_xl[g + d][r], wd = M == -INFINITY ? 0.f : ex2_approx(s_xm[g + d][r] - M);
-        s_xm[g + d][r] = wd;
-        if (ld != -1.f) l = fmaf(wd, ld, l);
+        const float ld = s_xl[g + d][r], below = M == -INFINITY ? -INFINITY : s_xm[g + d][r] - M;
+        s_xm[g + d][r] = ex2_approx(below);
+        if (ld != -1.f) l += scale_sum(ld, below);
         nans |= s_xnan[g + d][r];
       }
       m = M;
@@ -922,7 +937,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
 #pragma unroll 4
         for (int i = c0; i <= c1; ++i) {
           const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(i) + 128 * DH + 2 * r));
-          L = fmaf(ex2_approx(ml.x - M), ml.y, L);
+          L += scale_sum(ml.y, ml.x - M);
         }
       }
       s_wm[g][r] = M;

@@ -186,6 +186,55 @@ def test_attention_magnitudes(dt, new):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("new", [[4], [40], [300]])
+@pytest.mark.parametrize("big", [0, 7, 14])
+def test_pages_of_very_small_values_keep_their_weight(dt, new, big):
+    """Equal scores; one page's values are 2^30, the others' zero with the
+    smallest scale: those weigh nothing in the sum of the values and as much as
+    any in the normaliser."""
+    c = Call(17, new, [1000], dt, q_std=0.0)
+    c.codes[:, 1] = 0
+    c.scales[:, 1] = 2.0 ** -100
+    c.codes[c.table[0, big], 1] = 0x38  # 1.0
+    c.scales[c.table[0, big], 1] = 2.0 ** 30
+    c.upload()
+    c.check()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("new", [[4], [40], [300]])
+def test_many_small_weights_beside_a_large_one(dt, new):
+    """Token 0 outweighs each other by e^18, about 2^26, and its value is zero:
+    the output is the sum of thousands of small weights.  Their errors: the
+    exponent's as in Call.bound for sums of |q k| / 8 up to 18; a weight 2^26
+    below the largest is held to 2^-11 in the first kernel, where the largest is
+    2^15, and to 2^-10 where the largest may be 2^11 and this one, 2^-15, lies
+    in fp16's subnormals (a step of 2^-24, half of it lost); in the fp32 build
+    the second half of a weight 2^-11 does, 2^-25 of it lost, 2^-14 relative; the
+    output's rounding."""
+    c = Call(18, new, [4096], dt)
+    qkv = c.qkv.copy()
+    qkv[:, :512] = 1.0
+    c.qkv_d = dev(qkv.astype(np.float32), tdt(dt))
+    c.codes[:] = 0
+    c.codes[:, 1] = 0x38  # 1.0
+    c.scales[:] = 1.0
+    first = c.table[0, 0]
+    c.codes[first, 0, :, 0, 0] = 0x71  # 144
+    c.codes[first, 1, :, :, 0] = 0
+    c.upload()
+    out, ws = c.attend()
+    torch.cuda.synchronize()
+    assert ptl.last_device_error(ws) == 0
+    others = (4096 + np.arange(c.T)).astype(np.float64)
+    ref = others * np.exp(-18.0) / (1 + others * np.exp(-18.0))
+    half, prob = (2.0 ** -8, 2.0 ** -10) if dt == "bf16" else (2.0 ** -24, 2.0 ** -14)
+    tol = half + prob + 2 * (67 * 2.0 ** -23 + 2.0 ** -22) * 18 + 2 * 2.0 ** -22 + 3 * 4400 * 2.0 ** -24
+    off = np.abs(host(out) / ref[:, None] - 1)
+    assert off.max() <= tol, (off.max(), tol)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
 @pytest.mark.parametrize("new,past", [([3, 1], [100, 700]), ([150, 40], [100, 700])])
 def test_masked_places_have_no_effect(dt, new, past):
     """NaN codes behind the last token, before the window, and in front of
