@@ -470,7 +470,8 @@ ptl_status ptl_partition_users(const int32_t* cu_seqlens, int32_t num_users, int
  * tokens 64 k .. 64 k + 63 of its sequence.  past_lens: device int32 [U], the
  * tokens of user u's sequence before this call; token i of user u in the call
  * stands at position past_lens[u] + i.  The tables belong to the caller;
- * ptl_kv_pool_* keeps them for it.  max_pages: 1 .. 2^25 - 1.
+ * ptl_kv_pool_* keeps them for it.  max_pages: 1 .. 2^25 - 1, num_users: 1 ..
+ * 2^30.
  *
  * ptl_kv_append writes the keys and values of qkv[T][1536] (columns 512..1535)
  * at their positions.  A touched page and side and head gets the scale

@@ -804,8 +804,8 @@ ptl_status ptl_kv_append(const void* qkv, const int32_t* cu_seqlens, int32_t num
                          const int32_t* past_lens, void* workspace, size_t ws_bytes, void* stream) {
   ApiRange nvtx_range{"ptl_kv_append"};
   if (dt != PTL_F32 && dt != PTL_BF16) return PTL_ERR_DTYPE;
-  if (total_tokens < 0 || total_tokens >= (int64_t(1) << 31) || num_users < 1 || max_pages < 1 ||
-      max_pages > KV_MAX_PAGES)
+  if (total_tokens < 0 || total_tokens >= (int64_t(1) << 31) || num_users < 1 ||
+      num_users > KV_MAX_USERS || max_pages < 1 || max_pages > KV_MAX_PAGES)
     return PTL_ERR_SHAPE;
   ptl_status s;
   if ((s = check_small_ws(workspace, ws_bytes, 256)) != PTL_OK) return s;
@@ -859,8 +859,8 @@ ptl_status ptl_attention_paged(const void* qkv, void* attn, const int32_t* cu_se
                                void* workspace, size_t ws_bytes, void* stream) {
   ApiRange nvtx_range{"ptl_attention_paged"};
   if (dt != PTL_F32 && dt != PTL_BF16) return PTL_ERR_DTYPE;
-  if (total_tokens < 0 || total_tokens >= (int64_t(1) << 31) || num_users < 1 || max_pages < 1 ||
-      max_pages > KV_MAX_PAGES)
+  if (total_tokens < 0 || total_tokens >= (int64_t(1) << 31) || num_users < 1 ||
+      num_users > KV_MAX_USERS || max_pages < 1 || max_pages > KV_MAX_PAGES)
     return PTL_ERR_SHAPE;
   if (sinks < 0) return PTL_ERR_BAD_MASK;
   ptl_status s;

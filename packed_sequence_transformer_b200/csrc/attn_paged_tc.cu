@@ -12,23 +12,32 @@
 //                 tile and take its pages in turn, in a one-tile unit all four
 //                 do; each has scores, weights and sums of its own, which are
 //                 added at the unit's end.  So each scheduler has four warps
-//                 whose waits and exponentials interleave: with two groups of
-//                 whole tiles the same steps took 2.4 times as long, the
-//                 groups in step with one another and the exponentials' unit
-//                 idle three quarters of the time.
+//                 whose waits and exponentials interleave: with two groups, each
+//                 with a tile to itself, 256 queries over each of 16
+//                 histories of 8,000 took 201 us where four took 160.
 //   warps 16..19  converters, two pairs: a pair takes every second page, brings
-//                 it into shared memory with asynchronous copies, one page of
-//                 its own ahead, and turns it into fp16 in the 128-byte-swizzled layout of the
-//                 MMA operands (exact; both sides are stored along the
-//                 contraction, so both are K-major); at a unit's start also
+//                 it into shared memory with asynchronous copies, two pages of
+//                 its own ahead, and turns it into fp16 in the 128-byte-swizzled
+//                 layout of the MMA operands (exact; both sides are stored along
+//                 the contraction, so both are K-major); at a unit's start also
 //                 its queries, brought to fp16 by a power of two per row.  The
 //                 first one also walks the block's units and lays down what
 //                 the roles need of each (PagedPart) in a ring in shared
 //                 memory, so that no other spends registers on it.
 //   warps 20..23  MMA issuers, one thread per group: per page S = Q K^T
 //                 (128 x 64), then O += P V with P from TMEM, where it has
-//                 taken S's place.
+//                 taken S's place.  The whole warp walks along and one lane
+//                 issues: with the other lanes parted from it a page's eight
+//                 products took 788 cycles instead of 543.
 //
+// What bounds it: the exponentials, and the chain from a page's scores to its
+// weights beside them.  A round of the four groups (each one page of its tile)
+// takes about 3,340 cycles, 2,048 of them the 128 x 64 exponentials of each
+// group at 16 a cycle; the products take 1,250 (eight a page, 128 x 64 x 16 in
+// about 39 cycles).
+// Measured: 16 users with 256 new tokens over 16,000: 244 us, 554 TFLOP/s; 100
+// of each of 60 users over 2,000: 103 us; 31 users' prompts of 1,419 tokens
+// (44,000 in all): 210 us; a call that begins and ends only, 35 to 40 us.
 //
 // Exponent: t = s q_row k_page + log2(v_page), w = 2^(t - m): the value scale,
 // a power of two, rides in the exponent, so that O accumulates over pages in
@@ -60,7 +69,7 @@ constexpr int PTC_THREADS = 32 * (PTC_ISSUE0 + PTC_GROUPS);
 constexpr int PTC_PARTS = 16;   // units in the plan's ring: converters ask for pages up to 4 units ahead
 // 24 warps, 80 registers each at launch, dealt out anew (6 * 80 = 4 * 88 + 88 +
 // 40): with 80 everywhere the loops spill, and a spilled register costs a trip
-// to L2 here, for shared memory takes nearly all of L1 (200 us instead of 160
+// to L2 here, for shared memory takes nearly all of L1 (168 us instead of 160
 // for 256 queries over each of 16 histories of 8,000 tokens).
 constexpr int PTC_REGS = 88, PTC_REGS_ISSUE = 40;
 constexpr int PTC_QB = 256;     // queries of a unit, two tiles of 128
@@ -153,7 +162,8 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // One unit and the pages of it that this block has.  Costs, not pages, are
 // laid end to end: a page of a two-tile unit counts 2, one of a one-tile unit 1
 // (measured 0.92 and 0.51 us), and a unit's first page PTC_UNIT more, what
-// beginning and ending a unit costs.  A page belongs to the block that its
+// beginning and ending a unit costs (31 prompts of 1,419 tokens: 229, 214, 208
+// and 208 us with 4, 8, 12 and 16).  A page belongs to the block that its
 // first cost falls into, and blocks have at least PTC_UNIT + 2 costs each, so
 // every block between a unit's first and last has a page of it.
 constexpr int PTC_UNIT = 12;

@@ -20,9 +20,16 @@ constexpr int KV_TILE = KV_PAGE * DH;       // bytes of one side of one head of 
 constexpr int KV_SIDE = H * KV_TILE;        // bytes of the keys (or the values) of a page
 constexpr int KV_PAGE_BYTES = 2 * KV_SIDE;  // 65536
 constexpr int KV_MIN_EXP = -100;            // smallest scale 2^-100
+// Users with at most this many new tokens take attn_paged.cu's kernel, which
+// reads the pages once for each 8 of them; the tcgen05 kernel reads them once
+// for 256, but works on 128 rows whether or not they are there.  Of 60 users
+// over 2,000 tokens each: 32 new ones 96 to 107 us in the first (25 us a group
+// of 8), 33 take 119 in the second and 40 take 118.  The fp32 build has the
+// first kernel only: fp16 operands hold no fp32 query in one part.
 constexpr int PAGED_FEW = 32;
 constexpr int PAGED_TC_MAX_CTAS = 148;
 constexpr int PAGED_MAX_CTAS = 2 * 148;     // bound on the paged attention's grid (its workspace holds two parts per block)
+constexpr int KV_MAX_USERS = 1 << 30;       // a thread's range of users stays below 2^31
 constexpr int KV_MAX_PAGES = (1 << 25) - 1;  // pages of a sequence: positions stay below 2^31
 
 struct KvAppendArgs {

