@@ -36,24 +36,27 @@ int launch_kv_clear(void* ws, size_t bytes, cudaStream_t st) {
 // unless it falls into e4m3's subnormals; with any other scale each raise
 // would round every kept code once more.
 //
-// A block of 256 threads takes one (page, side, four heads) at a time: warp
-// (head, half) holds 32 tokens of one head in registers (one read of the
-// input), the two halves of a head meet in shared memory for the maximum, and
-// the codes leave from the registers.  One barrier an item: the next item is
-// looked up while this one's loads are under way.  Values are turned to [dim][token] on the way out: a
-// lane holds 4 consecutive tokens of 8 dims, so a 32-bit word of 4 tokens is
-// built in registers, and the words of a warp are exchanged through a
-// swizzled 2 KB tile (granule ^ dim / 8: the 8 lanes that store one word of 8
+// Two warps take one (page, side, head) at a time: each holds 32 tokens in
+// registers (one read of the input), they meet in shared memory for the maximum
+// over the 64, and the codes leave from the registers.  The pairs of a block run
+// apart from one another, so that loads of some fall into the conversions of
+// others; a pair looks its next item up while this one's loads are under way
+// (asking for its rows in L2 besides changed nothing).  Values are turned to
+// [dim][token] on the way out: a lane holds 4 consecutive tokens of 8 dims, so a
+// 32-bit word of 4 tokens is built in registers, and the words of a warp are
+// exchanged through a swizzled 2 KB tile (granule ^ dim / 8: the 8 lanes that store one word of 8
 // different rows hit 8 different 16-byte bank groups).
 // Every block works the list of pages out of the offsets by itself (a sum per
 // thread and a scan), which costs it a microsecond and saves a launch.  Block 0
 // only checks: it alone writes the error word, once, so that no launch before
 // this one has to clear it.
-// Measured: 60 users, one token each 8.3 us (launch, look-up and one item's
-// latency); 6,823 tokens 14 us; 44,000 tokens, 135 MB moved, 44 us, 47% of a
-// copy's rate, for a block has one item's loads in flight and then its stores.
+// Measured: 60 users, one token each 8.8 us (launch, look-up and one item's
+// latency); 6,823 tokens 13.9 us; 44,000 tokens, 135 MB moved, 40.5 us (with whole
+// blocks of 4 heads an item, 44): five rounds of load, convert and store with 32
+// warps an SM; more would have to do with 48 registers, which spills (43 us
+// where this takes 37).
 constexpr int KVA_THREADS = 256;
-constexpr int KVA_HEADS = KVA_THREADS / 64;  // heads of an item
+constexpr int KVA_PAIRS = KVA_THREADS / 64;
 
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
   uint32_t out = 0;
@@ -76,9 +79,8 @@ template <typename T>
 __global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 4 : 2) kv_append_kernel(const KvAppendArgs a) {
   constexpr int VEC = 16 / sizeof(T);   // elements of a 16-byte load
   constexpr int NLD = 8 / VEC;          // loads of a lane's 8 dims
-  __shared__ int64_t s_scan[KVA_THREADS / 32];
-  __shared__ uint32_t s_amax[2][KVA_HEADS][2];
-  __shared__ int s_item[2][4];
+  __shared__ int64_t s_scan[KVA_THREADS / 32], s_base[KVA_THREADS];
+  __shared__ uint32_t s_amax[2][KVA_PAIRS][2];
   __shared__ __align__(16) uint8_t s_turn[KVA_THREADS / 32][KV_TILE / 2];
   __shared__ int s_long[KVA_THREADS], s_longs;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -148,37 +150,42 @@ __global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 4 : 2) kv_append
     total += s_scan[w];
   }
 
-  // items: page, side, heads in that order, the page's parts next to one another
-  constexpr int PARTS = 2 * H / KVA_HEADS;
-  auto locate = [&](int64_t item, int* out) {
-    const int64_t ord = item / PARTS;
-    if (ord >= base && ord < base + mine) {  // one thread's users hold the page
-      int64_t left = ord - base;
-      for (int u = u_lo; u < u_hi; ++u) {
-        const int c0 = a.cu[u], n = a.cu[u + 1] - c0, p = a.past[u];
-        const int64_t cnt = n > 0 ? ((p + n - 1) >> 6) - (p >> 6) + 1 : 0;
-        if (left < cnt) {
-          const int pg = (p >> 6) + int(left);
-          const int r = left == 0 ? p & 63 : 0;        // tokens that the page keeps
-          const int t0 = left == 0 ? 0 : 64 * pg - p;  // first new token of the page
-          out[0] = a.table[int64_t(u) * a.max_pages + pg];
-          out[1] = r;
-          out[2] = min(64 - r, n - t0);
-          out[3] = c0 + t0;
-          break;
-        }
-        left -= cnt;
+  s_base[tid] = base;
+  __syncthreads();
+
+  // Items: page, side, head in that order, a page's next to one another.  Each
+  // warp looks its own up: whose range of users has the page (the last that
+  // begins at or before it), and which of those.
+  auto locate = [&](int64_t item, int& page, int& r, int& m, int& row0) {
+    const int64_t ord = item / (2 * H);
+    constexpr int STEP = KVA_THREADS / 32;
+    const int w = __popc(__ballot_sync(0xffffffffu, s_base[lane * STEP] <= ord)) - 1;
+    const int k = w * STEP + __popc(__ballot_sync(0xffffffffu, lane < STEP && s_base[w * STEP + lane % STEP] <= ord)) - 1;
+    int64_t left = ord - s_base[k];
+    for (int u = k * per;; ++u) {
+      const int c0 = a.cu[u], n = a.cu[u + 1] - c0, p = a.past[u];
+      const int64_t cnt = n > 0 ? ((p + n - 1) >> 6) - (p >> 6) + 1 : 0;
+      if (left < cnt) {
+        const int pg = (p >> 6) + int(left);
+        const int t0 = left == 0 ? 0 : 64 * pg - p;  // first new token of the page
+        r = left == 0 ? p & 63 : 0;                  // tokens that the page keeps
+        page = a.table[int64_t(u) * a.max_pages + pg];
+        m = min(64 - r, n - t0);
+        row0 = c0 + t0;
+        break;
       }
+      left -= cnt;
     }
   };
   int cur = 0;
-  const int block = blockIdx.x - 1, blocks = gridDim.x - 1;
-  if (int64_t(block) < PARTS * total) locate(block, s_item[0]);
-  __syncthreads();
-  for (int64_t it = block; it < PARTS * total; it += blocks, cur ^= 1) {
-    const int sub = int(it % PARTS), side = sub / (H / KVA_HEADS);
-    const int head = (sub % (H / KVA_HEADS)) * KVA_HEADS + (warp >> 1);
-    const int page = s_item[cur][0], r = s_item[cur][1], m = s_item[cur][2], row0 = s_item[cur][3];
+  const int pair = warp >> 1;
+  const int64_t items = 2 * H * total, stride = int64_t(gridDim.x - 1) * KVA_PAIRS;
+  int64_t it = int64_t(blockIdx.x - 1) * KVA_PAIRS + pair;
+  int page_n = 0, r_n = 0, m_n = 0, row0_n = 0;
+  if (it < items) locate(it, page_n, r_n, m_n, row0_n);
+  for (; it < items; it += stride, cur ^= 1) {
+    const int side = int(it % (2 * H)) / H, head = int(it % H);
+    const int page = page_n, r = r_n, m = m_n, row0 = row0_n;
     const bool ok = page >= 0 && page < a.num_pages;  // (block 0 reports it)
 
     // 32 tokens (8 per lane: two groups of 4 consecutive ones) x 8 dims
@@ -193,7 +200,7 @@ __global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 4 : 2) kv_append
         raw[i * NLD + k] = has ? __ldcs(reinterpret_cast<const uint4*>(in + int64_t(row0 + t - r) * QKV_N + k * VEC))
                                : make_uint4(0, 0, 0, 0);
     }
-    if (it + blocks < PARTS * total) locate(it + blocks, s_item[cur ^ 1]);
+    if (it + stride < items) locate(it + stride, page_n, r_n, m_n, row0_n);
     // largest finite magnitude; NaN and infinities count as NaN.  As integers
     // magnitudes are ordered like the numbers; anything not finite is taken out
     // in a second look that ordinary inputs never need.
@@ -228,12 +235,12 @@ __global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 4 : 2) kv_append
         }
       mx = __reduce_max_sync(0xffffffffu, mx);
     }
-    if (lane == 0) s_amax[cur][warp >> 1][half] = mx;
+    if (lane == 0) s_amax[cur][pair][half] = mx;
     float* sp = a.scales + (int64_t(ok ? page : 0) * 2 + side) * H + head;
     const float s_old = r > 0 ? *sp : 0.f;
-    __syncthreads();
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
     if (!ok) continue;  // (uniform)
-    mx = max(s_amax[cur][warp >> 1][0], s_amax[cur][warp >> 1][1]);
+    mx = max(s_amax[cur][pair][0], s_amax[cur][pair][1]);
     // smallest k with max |x| <= 448 * 2^k = 1.75 * 2^(k + 8)
     const int ke = max(int((mx + 0x1FFFFFu) >> 23) - 127 - 8, KV_MIN_EXP);
     const float s = fmaxf(s_old, __uint_as_float(uint32_t(ke + 127) << 23));
@@ -330,7 +337,7 @@ __global__ void __launch_bounds__(KVA_THREADS, sizeof(T) == 2 ? 4 : 2) kv_append
 int launch_kv_append(const KvAppendArgs& a, ptl_dtype dt, cudaStream_t st) {
   // at most T / 64 + 2 pages per user with tokens are touched, two sides each
   const int64_t users = a.U < a.T ? a.U : a.T;
-  const int64_t items = 2 * H / KVA_HEADS * (a.T / KV_PAGE + 2 * users);
+  const int64_t items = 2 * H / KVA_PAIRS * (a.T / KV_PAGE + 2 * users);
   const int64_t most = int64_t(num_sms()) * (dt == PTL_BF16 ? 4 : 2);
   const dim3 grid(unsigned(items < most ? items : most) + 1);
   const int r = dt == PTL_BF16 ? launch_k(kv_append_kernel<__nv_bfloat16>, grid, dim3(KVA_THREADS), 0, st, a)
