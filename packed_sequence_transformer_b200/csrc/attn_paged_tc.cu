@@ -281,7 +281,9 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
   uint8_t* sRaw = sKV + PTC_STAGES * PTC_STAGE;        // [converter pair][raw stage]
   __shared__ uint64_t q_full[2], q_empty[2], kv_full[PTC_STAGES], kv_empty[PTC_STAGES];
   __shared__ uint64_t s_full[PTC_GROUPS], p_full[PTC_GROUPS], o_full[PTC_GROUPS], o_empty[PTC_GROUPS];
-  __shared__ uint64_t x_full[PTC_GROUPS], x_empty[PTC_GROUPS], group_bar[PTC_GROUPS];
+  // (who adds group 3's sums up depends on the unit's kind: a barrier for each,
+  // so that each waits for every phase of the one that it looks at)
+  __shared__ uint64_t x_full[2][PTC_GROUPS], x_empty[PTC_GROUPS], group_bar[PTC_GROUPS];
   __shared__ float s_rawscale[2][PTC_RAW][2];
   // [stage] key scale, value scale's log2 and reciprocal, page number * 4 with
   // bits 0 and 1: tile 0's and 1's queries all see all of it
@@ -312,7 +314,8 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
       mbar_init(&p_full[i], 128);
       mbar_init(&o_full[i], 1);
       mbar_init(&o_empty[i], 128);
-      mbar_init(&x_full[i], 128);
+      mbar_init(&x_full[0][i], 128);
+      mbar_init(&x_full[1][i], 128);
       mbar_init(&x_empty[i], 128);
       mbar_init(&group_bar[i], 128);
     }
@@ -852,7 +855,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
         s_xl[g][r] = pages > 0 ? l : -1.f;  // -1: no page, no O
         s_xnan[g][r] = nans;
         tc_fence_before();
-        mbar_arrive(&x_full[g]);
+        mbar_arrive(&x_full[two][g]);
         continue;
       }
       const int donors = two ? 1 : 3, row_base = u.row0 + 128 * tile, c0 = u.c0, c1 = u.c1;
@@ -861,7 +864,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
       float M = m;
 #pragma unroll 1
       for (int d = 1; d <= donors; ++d) {
-        if (!warp_wait_bar(&x_full[g + d], handed(g + d) & 1)) {
+        if (!warp_wait_bar(&x_full[two][g + d], (two ? unit - singles : singles - 1) & 1)) {
           ok = false;
           break;
         }

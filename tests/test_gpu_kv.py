@@ -185,6 +185,26 @@ def test_attention_magnitudes(dt, new):
     c.check()
 
 
+@pytest.mark.parametrize("new,past,window,sinks", [
+    ([50, 140, 33], [5000, 3000, 0], 2900, 100), ([140, 60, 200, 40, 300], [10, 700, 0, 300, 100], 0, 0),
+    ([129, 128, 257, 33, 512] * 4, [0, 64, 3, 500, 0] * 4, 0, 0)])
+def test_attention_same_bits_every_time(new, past, window, sinks):
+    """Blocks that go from users with one tile of queries to users with two and
+    back: whoever is ahead waits for the others, call after call."""
+    c = Call(34, new, past)
+    first = c.check(window, sinks)
+    ws = ptl.attention_paged_workspace(c.T, len(new), "bf16")
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    other = torch.empty(32 << 20, dtype=torch.uint8, device="cuda")
+    for i in range(300):
+        if i % 3 == 0:
+            other.fill_(i & 255)
+        out, _ = c.attend(window, sinks, ws=ws)
+        differ += (out.view(torch.int16) != first.view(torch.int16)).any()
+    assert differ.item() == 0
+    assert ptl.last_device_error(ws) == 0
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
 @pytest.mark.parametrize("new", [[4], [40], [300]])
 @pytest.mark.parametrize("big", [0, 7, 14])
