@@ -111,6 +111,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -528,6 +529,9 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
         const bool has = row < u.rows;
 #pragma unroll
         for (int c = 0; c < 8; ++c) x[c] = has ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        // into L2 meanwhile: the second tile's row, the next head's
+        if (i == 0 && row + 128 < u.rows) prefetch_l2(src + 128 * (QKV_N / 8));
+        if (has && u.head + 1 < H) prefetch_l2(src + 8);
         uint32_t mx = 0;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -945,13 +949,13 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
       float L = 0.f;
       if (r < rows) {
 #pragma unroll 4
-        for (int i = c0; i <= c1; ++i) M = fmaxf(M, __ldcg(part(i) + 128 * DH + 2 * r));
-        if (M == -INFINITY) M = 0.f;
-#pragma unroll 4
         for (int i = c0; i <= c1; ++i) {
           const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(i) + 128 * DH + 2 * r));
-          L += scale_sum(ml.y, ml.x - M);
+          const float mn = fmaxf(M, ml.x), ref = mn == -INFINITY ? 0.f : mn;
+          L = scale_sum(L, M - ref) + scale_sum(ml.y, ml.x - ref);
+          M = mn;
         }
+        if (M == -INFINITY) M = 0.f;
       }
       s_wm[g][r] = M;
       s_wl[g][r] = 1.0f / L;
