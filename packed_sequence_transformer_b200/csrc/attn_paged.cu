@@ -49,7 +49,12 @@ using namespace sm100;
 
 constexpr int PA_THREADS = 32 * H;
 constexpr int PA_QG = 8;        // queries of a unit
-constexpr int PA_PARTS = 128;   // blocks that share a unit, at most about
+// Blocks that share a unit of k pages, at most about PA_PARTS sqrt(k): a step
+// takes the blocks 1.3 us each and a part the one that adds them up 0.15 us (one
+// query) to 0.6 us (eight), and the sum k / parts * step + parts * part is least
+// near there.  One user over 8,000: one query 28 us, with 128 parts 46; eight
+// queries 50 us, with 128 parts 153.
+constexpr float PA_PARTS_ONE = 4.f, PA_PARTS = 1.5f;
 // 4 KB tiles in a warp's ring, about 190 KB an SM: two blocks of the bf16 build,
 // one of the fp32 build, whose two-part operands need the registers of both
 // (with two blocks it spilled: 36 us instead of 26 for 5 new tokens of 60 users
@@ -102,6 +107,7 @@ struct Count {
 // A position in the call's (unit, page) steps.
 struct PagedWalk {
   int u, q0, n, past, k;
+  int few;        // users with at most this many new tokens count
   int64_t start;  // step of the unit's first page
   PageSpan span;
   __device__ __forceinline__ void load(const PagedArgs& a) {
@@ -125,16 +131,16 @@ struct PagedWalk {
       do {
         ++u;
         load(a);
-      } while (n == 0 || n > a.few);
+      } while (n == 0 || n > few);
     }
     see(a);
   }
 };
 
 // Steps of one user.
-__device__ __forceinline__ int64_t paged_user_steps(const PagedArgs& a, int n, int past) {
+__device__ __forceinline__ int64_t paged_user_steps(const PagedArgs& a, int n, int past, int few) {
   int64_t s = 0;
-  if (n > a.few) return 0;
+  if (n > few) return 0;
   for (int q0 = 0; q0 < n; q0 += PA_QG)
     s += page_span(past + q0, past + min(q0 + PA_QG, n) - 1, a.window, a.sinks).count;
   return s;
@@ -145,7 +151,7 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS<SPLIT>) attn_paged_kerne
   constexpr int STAGES = PA_STAGES<SPLIT>;
   extern __shared__ __align__(128) uint8_t ring_all[];
   __shared__ uint64_t s_bar[H][STAGES];
-  __shared__ int64_t s_scan[H];
+  __shared__ int64_t s_scan[H], s_many[2][H];
   __shared__ int s_longest[H];
   __shared__ int s_first[3];
   __shared__ PagedWalk s_walk[H][2];
@@ -163,16 +169,22 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS<SPLIT>) attn_paged_kerne
   // every block counts the call's steps by itself: a sum per thread, a scan
   const int per = (a.U + PA_THREADS - 1) / PA_THREADS;
   const int u_lo = min(tid * per, a.U), u_hi = min(u_lo + per, a.U);
-  int64_t mine = 0;
-  int longest = 0;  // pages of the longest unit
+  int few = a.few;
+  int64_t mine = 0, many_steps = 0, many_cost = 0;
+  int longest = 0;  // pages of the longest unit, twice, and 1 if its user has several queries
   int bad = 0;
+  auto count = [&](int n, int p) {
+    mine += paged_user_steps(a, n, p, few);
+    longest = max(longest, 2 * page_span(p + (n - 1) / PA_QG * PA_QG, p + n - 1, a.window, a.sinks).count + (n > 1));
+  };
   for (int u = u_lo; u < u_hi; ++u) {
     int n, p;
     const int e = kv_check_user(a.cu, a.past, u, a.U, a.T, a.max_pages, n, p);
     bad |= e == 0 ? 0 : e == PTL_ERR_BAD_OFFSETS ? 1 : 2;
-    if (e == 0 && n > 0 && n <= a.few) {
-      mine += paged_user_steps(a, n, p);
-      longest = max(longest, page_span(p + (n - 1) / PA_QG * PA_QG, p + n - 1, a.window, a.sinks).count);
+    if (e == 0 && n > 0 && n <= few) count(n, p);
+    if (e == 0 && n > few) {
+      many_steps += paged_few_steps(a, n, p);
+      many_cost += paged_tc_user_cost(a, n, p);
     }
   }
   if (__syncthreads_or(bad)) {  // every block sees the same offsets: nothing is written
@@ -181,29 +193,59 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS<SPLIT>) attn_paged_kerne
     if (blockIdx.x == 0 && tid == 0) set_error(a.err, offsets ? PTL_ERR_BAD_OFFSETS : PTL_ERR_BAD_PAGE);
     return;
   }
-  int64_t incl = mine;
+  int64_t base, W;
+  auto scan = [&]() {
+    int64_t incl = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 31) {
-    s_scan[warp] = incl;
-    s_longest[warp] = longest;
-  }
-  __syncthreads();
-  int64_t base = incl - mine, W = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 31) {
+      s_scan[warp] = incl;
+      s_longest[warp] = longest;
+    }
+    __syncthreads();
+    base = incl - mine;
+    W = 0;
 #pragma unroll
-  for (int w = 0; w < H; ++w) {
-    if (w < warp) base += s_scan[w];
-    W += s_scan[w];
-    longest = max(longest, s_longest[w]);
+    for (int w = 0; w < H; ++w) {
+      if (w < warp) base += s_scan[w];
+      W += s_scan[w];
+      longest = max(longest, s_longest[w]);
+    }
+  };
+  if (a.T > few) {  // (bf16) users with many new tokens: whose are they?
+    many_steps = warp_sum(many_steps);
+    many_cost = warp_sum(many_cost);
+    if (lane == 0) {
+      s_many[0][warp] = many_steps;
+      s_many[1][warp] = many_cost;
+    }
   }
-  // this block's steps [A, B); so few blocks that no unit falls into more than
-  // PA_PARTS (one block adds them up)
+  scan();
+  if (a.T > few) {
+    many_steps = many_cost = 0;
+#pragma unroll
+    for (int w = 0; w < H; ++w) {
+      many_steps += s_many[0][w];
+      many_cost += s_many[1][w];
+    }
+    if (many_steps > 0 && paged_all_few(many_steps, many_cost)) {  // this kernel's: counted again
+      few = INT32_MAX;
+      for (int u = u_lo; u < u_hi; ++u) {
+        const int n = a.cu[u + 1] - a.cu[u];
+        if (n > a.few) count(n, a.past[u]);
+      }
+      __syncthreads();
+      scan();
+    }
+  }
+  // this block's steps [A, B), in so few blocks that no unit falls into too many
   int64_t G = W < int64_t(gridDim.x) ? W : int64_t(gridDim.x);
-  if (longest > PA_PARTS && G * longest > PA_PARTS * W) G = PA_PARTS * W / longest;
+  const int64_t pages = longest >> 1, parts = int(sqrtf(float(pages)) * ((longest & 1) ? PA_PARTS : PA_PARTS_ONE));
+  if (G * pages > parts * W) G = parts * W / pages;
   if (int64_t(blockIdx.x) >= G) {
     pdl_wait();
     return;
@@ -221,7 +263,7 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS<SPLIT>) attn_paged_kerne
     int64_t left = A - base;
     for (int u = u_lo; u < u_hi; ++u) {
       const int n = a.cu[u + 1] - a.cu[u], p = a.past[u];
-      const int64_t s = paged_user_steps(a, n, p);
+      const int64_t s = paged_user_steps(a, n, p, few);
       if (left >= s) {
         left -= s;
         continue;
@@ -248,6 +290,7 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS<SPLIT>) attn_paged_kerne
   PagedWalk& cw = s_walk[warp][0];
   PagedWalk& iw = s_walk[warp][1];
   if (lane == 0) {
+    cw.few = few;
     cw.u = s_first[0];
     cw.q0 = s_first[1];
     cw.k = s_first[2];

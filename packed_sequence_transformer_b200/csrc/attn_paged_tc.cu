@@ -72,7 +72,6 @@ constexpr int PTC_PARTS = 16;   // units in the plan's ring: converters ask for 
 // to L2 here, for shared memory takes nearly all of L1 (168 us instead of 160
 // for 256 queries over each of 16 histories of 8,000 tokens).
 constexpr int PTC_REGS = 88, PTC_REGS_ISSUE = 40;
-constexpr int PTC_QB = 256;     // queries of a unit, two tiles of 128
 // Converted pages (keys and values of one head).  An even number: a stage then
 // belongs to one converter pair, whose order keeps its phases apart (a barrier's
 // parity cannot tell a phase from the one after next).
@@ -160,14 +159,10 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One unit and the pages of it that this block has.  Costs, not pages, are
-// laid end to end: a page of a two-tile unit counts 2, one of a one-tile unit 1
-// (measured 0.92 and 0.51 us), and a unit's first page PTC_UNIT more, what
-// beginning and ending a unit costs (31 prompts of 1,419 tokens: 229, 214, 208
-// and 208 us with 4, 8, 12 and 16).  A page belongs to the block that its
-// first cost falls into, and blocks have at least PTC_UNIT + 2 costs each, so
-// every block between a unit's first and last has a page of it.
-constexpr int PTC_UNIT = 12;
+// One unit and the pages of it that this block has.  Costs (paged_tc_user_cost),
+// not pages, are laid end to end.  A page belongs to the block that its first
+// cost falls into, and blocks have at least PTC_UNIT + 2 costs each, so every
+// block between a unit's first and last has a page of it.
 struct PagedTcUnit {
   int u, q0, head, n, past, k0, k1;
   bool two;
@@ -265,15 +260,6 @@ struct PagedPart {
   PagedTcTile tile[2];
 };
 
-__device__ __forceinline__ int64_t paged_tc_user_cost(const PagedArgs& a, int n, int past) {
-  int64_t s = 0;
-  if (n > a.few)
-    for (int q0 = 0; q0 < n; q0 += PTC_QB)
-      s += H * (PTC_UNIT + (int64_t(page_span(past + q0, past + min(q0 + PTC_QB, n) - 1, a.window, a.sinks).count)
-                            << (n - q0 > 128 ? 1 : 0)));
-  return s;
-}
-
 __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const PagedArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -296,7 +282,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
   __shared__ float s_xm[PTC_GROUPS][128], s_xl[PTC_GROUPS][128];  // maxima and sums handed over
   __shared__ uint64_t s_xnan[PTC_GROUPS][128];
   __shared__ float s_wm[PTC_GROUPS][128], s_wl[PTC_GROUPS][128];  // of the rows whose parts are added
-  __shared__ int64_t s_scan[PTC_THREADS / 32];
+  __shared__ int64_t s_scan[PTC_THREADS / 32], s_few[PTC_THREADS / 32];
   __shared__ int64_t s_start;
   __shared__ int s_first[3];
   __shared__ int s_done[PTC_GROUPS];
@@ -335,14 +321,16 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
   // the call's costs, counted by every block (see attn_paged.cu)
   const int per = (a.U + PTC_THREADS - 1) / PTC_THREADS;
   const int u_lo = min(tid * per, a.U), u_hi = min(u_lo + per, a.U);
-  int64_t mine = 0;
+  int64_t mine = 0, few_steps = 0;
   int bad = 0;
   for (int u = u_lo; u < u_hi; ++u) {
     int n, p;
     if (kv_check_user(a.cu, a.past, u, a.U, a.T, a.max_pages, n, p) != 0)
       bad = 1;
-    else
+    else if (n > a.few) {
       mine += paged_tc_user_cost(a, n, p);
+      few_steps += paged_few_steps(a, n, p);
+    }
   }
   if (__syncthreads_or(bad)) {  // attn_paged_kernel reports it
     pdl_wait();
@@ -354,16 +342,22 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
     const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) s_scan[warp] = incl;
+  few_steps = warp_sum(few_steps);
+  if (lane == 31) {
+    s_scan[warp] = incl;
+    s_few[warp] = few_steps;
+  }
   __syncthreads();
   int64_t base = incl - mine, W = 0;
+  few_steps = 0;
 #pragma unroll
   for (int w = 0; w < PTC_THREADS / 32; ++w) {
     if (w < warp) base += s_scan[w];
     W += s_scan[w];
+    few_steps += s_few[w];
   }
-  const int64_t G = min(int64_t(gridDim.x), max(W / (PTC_UNIT + 2), min(W, int64_t(1))));
-  if (int64_t(blockIdx.x) >= G) {
+  const int64_t G = min(int64_t(gridDim.x), max(W / (PTC_UNIT + 2), int64_t(1)));
+  if (int64_t(blockIdx.x) >= G || W == 0 || paged_all_few(few_steps, W)) {
     pdl_wait();
     return;
   }
@@ -372,7 +366,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
     int64_t left = A - base;
     for (int u = u_lo; u < u_hi; ++u) {
       const int n = a.cu[u + 1] - a.cu[u], p = a.past[u];
-      const int64_t s = paged_tc_user_cost(a, n, p);
+      const int64_t s = n > a.few ? paged_tc_user_cost(a, n, p) : 0;
       if (left >= s) {
         left -= s;
         continue;

@@ -27,6 +27,7 @@ constexpr int KV_MIN_EXP = -100;            // smallest scale 2^-100
 // of 8), 33 take 119 in the second and 40 take 118.  The fp32 build has the
 // first kernel only: fp16 operands hold no fp32 query in one part.
 constexpr int PAGED_FEW = 32;
+constexpr int PAGED_FEW_STEPS = 1000;
 constexpr int PAGED_TC_MAX_CTAS = 148;
 constexpr int PAGED_MAX_CTAS = 2 * 148;     // bound on the paged attention's grid (its workspace holds two parts per block)
 constexpr int KV_MAX_USERS = 1 << 30;       // a thread's range of users stays below 2^31
@@ -85,6 +86,36 @@ __device__ __forceinline__ PageSpan page_span(int p0, int p1, int window, int si
     s.count = s.sinks + (p1 >> 6) - s.first + 1;
   }
   return s;
+}
+
+// Cost of a user's units in the tcgen05 kernel: a page of a two-tile unit counts
+// 2, one of a one-tile unit 1 (measured 0.92 and 0.51 us), and a unit's first page
+// PTC_UNIT more, what beginning and ending a unit costs (31 prompts of 1,419
+// tokens: 229, 214, 208 and 208 us with 4, 8, 12 and 16).
+constexpr int PTC_QB = 256;  // queries of a unit, two tiles of 128
+constexpr int PTC_UNIT = 12;
+__device__ __forceinline__ int64_t paged_tc_user_cost(const PagedArgs& a, int n, int past) {
+  int64_t s = 0;
+  for (int q0 = 0; q0 < n; q0 += PTC_QB)
+    s += H * (PTC_UNIT + (int64_t(page_span(past + q0, past + min(q0 + PTC_QB, n) - 1, a.window, a.sinks).count)
+                          << (n - q0 > 128 ? 1 : 0)));
+  return s;
+}
+// The same user's (8 queries, page) steps in the other kernel, about: as if all
+// groups saw what the middle one sees.
+__device__ __forceinline__ int64_t paged_few_steps(const PagedArgs& a, int n, int past) {
+  const int mid = past + (n >> 1);
+  return int64_t((n + 7) >> 3) * page_span(mid, mid, a.window, a.sinks).count;
+}
+// Does attn_paged.cu's kernel take the users with many new tokens as well?
+// (Decided by both kernels from the same sums over those users.)
+__device__ __forceinline__ bool paged_all_few(int64_t few_steps, int64_t tc_cost) {
+  return few_steps < PAGED_FEW_STEPS + (tc_cost >> 2);
+}
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
 }
 
 // Bit b: does the query at position `pos` see token 64 * page + b (base = 64 *
