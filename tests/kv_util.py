@@ -37,9 +37,12 @@ def make_table(rng, new, past, num_pages=None, width=None):
 
 
 class Call:
-    """One call's inputs, on the host and on the device."""
+    """One call's inputs, on the host and on the device.  `beside`: a last user
+    with that many new tokens, all of whose pages are one page, whose output is
+    not looked at; many of them send the others' long queries through the
+    kernel for many new tokens."""
 
-    def __init__(self, seed, new, past, dt="bf16", q_std=1.0, num_pages=None):
+    def __init__(self, seed, new, past, dt="bf16", q_std=1.0, num_pages=None, beside=0):
         rng = np.random.default_rng(seed)
         self.rng, self.dt, self.new, self.past = rng, dt, new, past
         self.cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
@@ -49,6 +52,17 @@ class Call:
         qkv = rng.standard_normal((self.T, 1536))
         qkv[:, :512] *= q_std
         self.qkv_d = dev(qkv.astype(np.float32), tdt(dt))
+        self.rows, self.users = self.T, len(new)
+        if beside:
+            self.T += beside
+            self.new, self.past = list(new) + [beside], list(past) + [0]
+            self.cu = np.append(self.cu, self.T).astype(np.int32)
+            table = np.full((self.users + 1, max(self.table.shape[1], -(-beside // 64))), -1, np.int32)
+            table[:-1, :self.table.shape[1]] = self.table
+            table[-1] = self.num_pages - 1
+            self.table = table
+            rest = torch.randn(beside, 1536, device="cuda", generator=torch.Generator("cuda").manual_seed(seed))
+            self.qkv_d = torch.cat([self.qkv_d, rest.to(self.qkv_d.dtype)])
         self.upload()
 
     def upload(self):
@@ -72,8 +86,10 @@ class Call:
         return out, ws
 
     def oracle(self, window=0, sinks=0):
-        return O.attention_paged(self.qkv[:, :512].reshape(-1, 8, 64), value_of_codes(self.kv.codes),
-                                 host(self.kv.scales), self.cu, self.table, self.past, window, sinks, details=True)
+        U = self.users
+        return O.attention_paged(self.qkv[:self.rows, :512].reshape(-1, 8, 64), value_of_codes(self.kv.codes),
+                                 host(self.kv.scales), self.cu[:U + 1], self.table[:U], self.past[:U], window, sinks,
+                                 details=True)
 
     def bound(self, ref, mag, smax, count):
         """How far an output may be from the exact one, elementwise.
@@ -101,7 +117,7 @@ class Call:
         torch.cuda.synchronize()
         assert ptl.last_device_error(ws) == 0
         ref, mag, smax, count = self.oracle(window, sinks)
-        got = host(out).reshape(ref.shape)
+        got = host(out[:self.rows]).reshape(ref.shape)
         off = np.abs(got - ref) - self.bound(ref, mag, smax, count)
         assert np.isfinite(got).all() == np.isfinite(ref).all()
         bad = ~((off <= 0) | (np.isnan(got) & np.isnan(ref)))

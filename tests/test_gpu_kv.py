@@ -133,18 +133,26 @@ def test_append_reports_and_leaves_the_rest():
 
 
 # ------------------------------------------------------------- attention
+# (dtype, new tokens of a user beside the others': Call)
+KINDS = [("bf16", 0), ("bf16", 16000), ("fp32", 0)]
 SHAPES = [
     ([1], [0]), ([1], [1]), ([1], [62]), ([1], [63]), ([1], [64]), ([1], [500]),
     ([3], [0]), ([8], [120]), ([9], [120]), ([17], [55]), ([70], [0]), ([200], [0]), ([129], [131]),
     ([0, 1, 0, 2, 90, 0], [77, 0, 0, 130, 10, 5]),
-    ([1] * 33, [7 * i for i in range(33)]),
+    ([1] * 33, [7 * i for i in range(33)]), ([33], [0]), ([256], [64]), ([257], [300]), ([600, 40], [1500, 61]),
 ]
 
 
-@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("dt,beside", KINDS)
 @pytest.mark.parametrize("new,past", SHAPES)
-def test_attention_against_the_oracle(dt, new, past):
-    Call(new[0] * 7 + past[0] + len(new), new, past, dt).check()
+def test_attention_against_the_oracle(dt, beside, new, past):
+    Call(new[0] * 7 + past[0] + len(new), new, past, dt, beside=beside).check()
+
+
+@pytest.mark.parametrize("window,sinks", [(63, 0), (64, 64), (65, 65), (100, 3), (128, 200), (300, 1000),
+                                          (2 ** 31 - 1, 0), (0, 7), (900, 130)])
+def test_attention_window_and_sinks_of_many_new_tokens(window, sinks):
+    Call(window % 1000 + sinks % 1000, [1, 5, 200, 0, 1, 130], [700, 64, 90, 9, 0, 319], beside=40000).check(window, sinks)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
@@ -154,15 +162,15 @@ def test_attention_window_and_sinks(dt, window, sinks):
     Call(window % 1000 + sinks % 1000, [1, 5, 200, 0, 1, 130], [700, 64, 90, 9, 0, 319], dt).check(window, sinks)
 
 
-@pytest.mark.parametrize("dt", ["bf16", "fp32"])
-def test_attention_many_parts(dt):
+@pytest.mark.parametrize("dt,beside", KINDS)
+def test_attention_many_parts(dt, beside):
     """One history over more blocks than the grid has, and users whose pages end
     inside a block's range."""
-    Call(11, [1], [20000], dt).check()
-    Call(12, [2, 1, 9, 1], [9000, 10, 4000, 12345], dt).check()
-    Call(13, [1, 1], [15000, 15000], dt).check(window=9000, sinks=70)
-    Call(31, [40], [12000], dt).check()
-    Call(32, [50, 140, 33], [5000, 3000, 0], dt).check(window=2900, sinks=100)
+    Call(11, [1], [20000], dt, beside=beside).check()
+    Call(12, [2, 1, 9, 1], [9000, 10, 4000, 12345], dt, beside=beside).check()
+    Call(13, [1, 1], [15000, 15000], dt, beside=beside).check(window=9000, sinks=70)
+    Call(31, [40], [12000], dt, beside=beside).check()
+    Call(32, [50, 140, 33], [5000, 3000, 0], dt, beside=beside).check(window=2900, sinks=100)
 
 
 def test_attention_many_users():
@@ -171,11 +179,11 @@ def test_attention_many_users():
     Call(14, rng.integers(0, 3, 700).tolist(), rng.integers(0, 150, 700).tolist()).check()
 
 
-@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("dt,beside", KINDS)
 @pytest.mark.parametrize("new", [[16, 6], [150, 40]])
-def test_attention_magnitudes(dt, new):
+def test_attention_magnitudes(dt, beside, new):
     """Rows of q from tiny to huge, scales far apart from page to page."""
-    c = Call(15, new, [200, 300], dt)
+    c = Call(15, new, [200, 300], dt, beside=beside)
     x = host(c.qkv_d).astype(np.float32)
     x[:, :512] *= (10.0 ** np.linspace(-30, 1, c.T))[:, None].astype(np.float32)
     x[3, :512] = 0.0
@@ -185,34 +193,35 @@ def test_attention_magnitudes(dt, new):
     c.check()
 
 
+@pytest.mark.parametrize("beside", [0, 16000])
 @pytest.mark.parametrize("new,past,window,sinks", [
     ([50, 140, 33], [5000, 3000, 0], 2900, 100), ([140, 60, 200, 40, 300], [10, 700, 0, 300, 100], 0, 0),
     ([129, 128, 257, 33, 512] * 4, [0, 64, 3, 500, 0] * 4, 0, 0)])
-def test_attention_same_bits_every_time(new, past, window, sinks):
+def test_attention_same_bits_every_time(beside, new, past, window, sinks):
     """Blocks that go from users with one tile of queries to users with two and
     back: whoever is ahead waits for the others, call after call."""
-    c = Call(34, new, past)
+    c = Call(34, new, past, beside=beside)
     first = c.check(window, sinks)
-    ws = ptl.attention_paged_workspace(c.T, len(new), "bf16")
+    ws = ptl.attention_paged_workspace(c.T, len(c.new), "bf16")
     differ = torch.zeros((), dtype=torch.int64, device="cuda")
     other = torch.empty(32 << 20, dtype=torch.uint8, device="cuda")
     for i in range(300):
         if i % 3 == 0:
             other.fill_(i & 255)
         out, _ = c.attend(window, sinks, ws=ws)
-        differ += (out.view(torch.int16) != first.view(torch.int16)).any()
+        differ += (out[:c.rows].view(torch.int16) != first[:c.rows].view(torch.int16)).any()
     assert differ.item() == 0
     assert ptl.last_device_error(ws) == 0
 
 
-@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("dt,beside", KINDS)
 @pytest.mark.parametrize("new", [[4], [40], [300]])
 @pytest.mark.parametrize("big", [0, 7, 14])
-def test_pages_of_very_small_values_keep_their_weight(dt, new, big):
+def test_pages_of_very_small_values_keep_their_weight(dt, beside, new, big):
     """Equal scores; one page's values are 2^30, the others' zero with the
     smallest scale: those weigh nothing in the sum of the values and as much as
     any in the normaliser."""
-    c = Call(17, new, [1000], dt, q_std=0.0)
+    c = Call(17, new, [1000], dt, q_std=0.0, beside=beside)
     c.codes[:, 1] = 0
     c.scales[:, 1] = 2.0 ** -100
     c.codes[c.table[0, big], 1] = 0x38  # 1.0
@@ -221,9 +230,9 @@ def test_pages_of_very_small_values_keep_their_weight(dt, new, big):
     c.check()
 
 
-@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("dt,beside", KINDS)
 @pytest.mark.parametrize("new", [[4], [40], [300]])
-def test_many_small_weights_beside_a_large_one(dt, new):
+def test_many_small_weights_beside_a_large_one(dt, beside, new):
     """Token 0 outweighs each other by e^18, about 2^26, and its value is zero:
     the output is the sum of thousands of small weights.  Their errors: the
     exponent's as in Call.bound for sums of |q k| / 8 up to 18; a weight 2^26
@@ -232,7 +241,7 @@ def test_many_small_weights_beside_a_large_one(dt, new):
     in fp16's subnormals (a step of 2^-24, half of it lost); in the fp32 build
     the second half of a weight 2^-11 does, 2^-25 of it lost, 2^-14 relative; the
     output's rounding."""
-    c = Call(18, new, [4096], dt)
+    c = Call(18, new, [4096], dt, beside=beside)
     qkv = c.qkv.copy()
     qkv[:, :512] = 1.0
     c.qkv_d = dev(qkv.astype(np.float32), tdt(dt))
@@ -246,20 +255,20 @@ def test_many_small_weights_beside_a_large_one(dt, new):
     out, ws = c.attend()
     torch.cuda.synchronize()
     assert ptl.last_device_error(ws) == 0
-    others = (4096 + np.arange(c.T)).astype(np.float64)
+    others = (4096 + np.arange(c.rows)).astype(np.float64)
     ref = others * np.exp(-18.0) / (1 + others * np.exp(-18.0))
     half, prob = (2.0 ** -8, 2.0 ** -10) if dt == "bf16" else (2.0 ** -24, 2.0 ** -14)
     tol = half + prob + 2 * (67 * 2.0 ** -23 + 2.0 ** -22) * 18 + 2 * 2.0 ** -22 + 3 * 4400 * 2.0 ** -24
-    off = np.abs(host(out) / ref[:, None] - 1)
+    off = np.abs(host(out[:c.rows]) / ref[:, None] - 1)
     assert off.max() <= tol, (off.max(), tol)
 
 
-@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("dt,beside", KINDS)
 @pytest.mark.parametrize("new,past", [([3, 1], [100, 700]), ([150, 40], [100, 700])])
-def test_masked_places_have_no_effect(dt, new, past):
+def test_masked_places_have_no_effect(dt, beside, new, past):
     """NaN codes behind the last token, before the window, and in front of
     later queries; visible ones reach the queries that see them."""
-    c = Call(16, new, past, dt)
+    c = Call(16, new, past, dt, beside=beside)
     nan = np.uint8(0x7F)
     # behind the end
     for u in range(2):
@@ -279,6 +288,14 @@ def test_masked_places_have_no_effect(dt, new, past):
     c.check(window=21, sinks=1)
     c.check(window=20, sinks=1)
     c.check()
+    # the same for longer windows
+    at = past[1] - 140
+    page = c.table[1, at // 64]
+    c.codes[page, 1, 5, 7, at % 64] = nan
+    c.codes[page, 0, 4, at % 64, 63] = nan
+    c.upload()
+    for window in (151, 141, 140):
+        c.check(window=window, sinks=1)
     # in a row of the call itself: later queries see it, earlier ones do not
     at = past[0] + new[0] - 2
     page = c.table[0, at // 64]
@@ -288,21 +305,24 @@ def test_masked_places_have_no_effect(dt, new, past):
     assert torch.isnan(out[new[0] - 2:new[0], 0]).all() and torch.isfinite(out[:new[0] - 2, 0]).all()
 
 
-def test_infinite_queries_stay_in_their_rows():
-    c = Call(17, [4, 1], [90, 90])
+@pytest.mark.parametrize("beside", [0, 16000])
+def test_infinite_queries_stay_in_their_rows(beside):
+    n = 40 if beside else 4
+    c = Call(17, [n, 1], [90, 90], beside=beside)
     c.qkv_d[1, 70] = float("inf")
     c.qkv_d[2, 3] = float("nan")
     c.upload()
     out, ws = c.attend()
     torch.cuda.synchronize()
-    bad = torch.isnan(out.view(5, 8, 64)).all(-1).cpu().numpy()
-    want = np.zeros((5, 8), bool)
+    bad = torch.isnan(out[:n + 1].view(n + 1, 8, 64)).all(-1).cpu().numpy()
+    want = np.zeros((n + 1, 8), bool)
     want[1, 1] = want[2, 0] = True
     assert np.array_equal(bad, want)
 
 
-def test_attention_bad_page_is_reported():
-    c = Call(18, [1, 2], [300, 10])
+@pytest.mark.parametrize("beside", [0, 16000])
+def test_attention_bad_page_is_reported(beside):
+    c = Call(18, [40 if beside else 1, 2], [300, 10], beside=beside)
     good = c.table.copy()
     for bad in (-1, c.num_pages, 2 ** 31 - 1, -2 ** 31):
         c.table = good.copy()
@@ -327,11 +347,12 @@ def test_two_users_of_a_call_share_pages():
 
 
 # ------------------------------------------------------ streams and graphs
-@pytest.mark.parametrize("dt", ["bf16", "fp32"])
-def test_same_bits_on_other_streams_and_in_graphs(dt):
+@pytest.mark.parametrize("dt,beside", KINDS)
+def test_same_bits_on_other_streams_and_in_graphs(dt, beside):
     """Two calls under way at once, each with its workspace; two graphs that
     share one, replayed in turn, on new inputs."""
-    a, b = Call(20, [1, 7, 90], [4000, 50, 0], dt), Call(21, [2, 1, 33], [10, 9000, 200], dt)
+    a, b = (Call(20, [1, 7, 90], [4000, 50, 0], dt, beside=beside),
+            Call(21, [2, 1, 33], [10, 9000, 200], dt, beside=beside))
     want = [c.check().clone() for c in (a, b)]
     streams = [torch.cuda.Stream() for _ in range(2)]
     wss = [ptl.attention_paged_workspace(c.T, 3, dt) for c in (a, b)]
