@@ -30,14 +30,14 @@
 //                 issues: with the other lanes parted from it a page's eight
 //                 products took 788 cycles instead of 543.
 //
-// What bounds it: the exponentials, and the chain from a page's scores to its
-// weights beside them.  A round of the four groups (each one page of its tile)
-// takes about 3,340 cycles, 2,048 of them the 128 x 64 exponentials of each
-// group at 16 a cycle; the products take 1,250 (eight a page, 128 x 64 x 16 in
-// about 39 cycles).
-// Measured: 16 users with 256 new tokens over 16,000: 244 us, 554 TFLOP/s; 100
-// of each of 60 users over 2,000: 103 us; 31 users' prompts of 1,419 tokens
-// (44,000 in all): 210 us; a call that begins and ends only, 35 to 40 us.
+// What bounds it: the groups' chains from a page's scores to its weights, its
+// product and the next scores.  A round of the four groups takes about 3,400
+// cycles, of which the exponentials fill 2,048 and the products 1,250; with the
+// conversions, the exponentials, the maximum or three quarters of the products
+// left out it is at most 7% shorter each, with all of the softmax left out 50%.
+// Measured: 16 users with 256 new tokens over 16,000: 244 us, 554 TFLOP/s; 100 of
+// each of 60 users over 2,000: 103 us; 31 users' prompts of 1,419 tokens (44,000
+// in all): 206 us; a call that only begins and ends, 25 us.
 //
 // Exponent: t = s q_row k_page + log2(v_page), w = 2^(t - m): the value scale,
 // a power of two, rides in the exponent, so that O accumulates over pages in

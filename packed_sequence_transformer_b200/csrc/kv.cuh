@@ -24,8 +24,8 @@ constexpr int KV_MIN_EXP = -100;            // smallest scale 2^-100
 // reads the pages once for each 8 of them; the tcgen05 kernel reads them once
 // for 256, but works on 128 rows whether or not they are there.  Of 60 users
 // over 2,000 tokens each: 32 new ones 96 to 107 us in the first (25 us a group
-// of 8), 33 take 119 in the second and 40 take 118.  The fp32 build has the
-// first kernel only: fp16 operands hold no fp32 query in one part.
+// of 8), 33 take 99 in the second.  The fp32 build has the first kernel only:
+// fp16 operands hold no fp32 query in one part.
 constexpr int PAGED_FEW = 32;
 constexpr int PAGED_FEW_STEPS = 1000;
 constexpr int PAGED_TC_MAX_CTAS = 148;
@@ -108,7 +108,12 @@ __device__ __forceinline__ int64_t paged_few_steps(const PagedArgs& a, int n, in
   return int64_t((n + 7) >> 3) * page_span(mid, mid, a.window, a.sinks).count;
 }
 // Does attn_paged.cu's kernel take the users with many new tokens as well?
-// (Decided by both kernels from the same sums over those users.)
+// (Decided by both kernels from the same sums over those users.)  The tcgen05
+// kernel needs 25 us to begin and end, which a call with few steps does not earn
+// back.  First kernel / tcgen05 kernel, us: one user's 100 new tokens 20 / 25, 300
+// 26 / 43, 900 44 / 52; 60 users' 100 each 38 / 50, 40 over 500 48 / 58; 20 users'
+// 64 over 500 40 / 40; the other way, 20 users' 300 each 54 / 50, 500 of two over
+// 2,000 68 / 52, 33 of 30 over 4,000 112 / 93, 900 of ten 144 / 67.
 __device__ __forceinline__ bool paged_all_few(int64_t few_steps, int64_t tc_cost) {
   return few_steps < PAGED_FEW_STEPS + (tc_cost >> 2);
 }
