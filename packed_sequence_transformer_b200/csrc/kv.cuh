@@ -102,8 +102,11 @@ __device__ __forceinline__ int64_t paged_tc_user_cost(const PagedArgs& a, int n,
   return s;
 }
 // The same user's (8 queries, page) steps in the other kernel, about: as if all
-// groups saw what the middle one sees.
+// groups saw what the middle one sees.  A user with more than 1,024 new tokens
+// counts as too many for a whole call: one thread counts a user's groups one by
+// one (a sum over all users stays below 2^63).
 __device__ __forceinline__ int64_t paged_few_steps(const PagedArgs& a, int n, int past) {
+  if (n > 1024) return int64_t(1) << 40;
   const int mid = past + (n >> 1);
   return int64_t((n + 7) >> 3) * page_span(mid, mid, a.window, a.sinks).count;
 }

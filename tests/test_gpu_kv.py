@@ -155,6 +155,11 @@ def test_attention_window_and_sinks_of_many_new_tokens(window, sinks):
     Call(window % 1000 + sinks % 1000, [1, 5, 200, 0, 1, 130], [700, 64, 90, 9, 0, 319], beside=40000).check(window, sinks)
 
 
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 4), (63, 0), (5, 2 ** 31 - 1), (64, 64), (-4, 0)])
+def test_attention_small_windows_of_a_long_prompt(window, sinks):
+    Call(window % 1000 + 1, [140, 1100, 3, 33], [77, 0, 200, 640]).check(window, sinks)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 4), (63, 0), (64, 64), (65, 65), (100, 3), (128, 200),
                                           (5, 2 ** 31 - 1), (2 ** 31 - 1, 0), (300, 1000), (0, 7), (-4, 0)])
