@@ -167,35 +167,39 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS<SPLIT>) attn_paged_kerne
   }
   pdl_trigger();
 
-  // every block counts the call's steps by itself: a sum per thread, a scan
+  // every block counts the call's steps by itself: a sum per thread, a scan; and
+  // once more if users with many new tokens turn out to be this kernel's as well
   const int per = (a.U + PA_THREADS - 1) / PA_THREADS;
   const int u_lo = min(tid * per, a.U), u_hi = min(u_lo + per, a.U);
   int few = a.few;
-  int64_t mine = 0, many_steps = 0, many_cost = 0;
-  int longest = 0;  // pages of the longest unit, twice, and 1 if its user has several queries
-  int bad = 0;
-  auto count = [&](int n, int p) {
-    mine += paged_user_steps(a, n, p, few);
-    longest = max(longest, 2 * page_span(p + (n - 1) / PA_QG * PA_QG, p + n - 1, a.window, a.sinks).count + (n > 1));
-  };
-  for (int u = u_lo; u < u_hi; ++u) {
-    int n, p;
-    const int e = kv_check_user(a.cu, a.past, u, a.U, a.T, a.max_pages, n, p);
-    bad |= e == 0 ? 0 : e == PTL_ERR_BAD_OFFSETS ? 1 : 2;
-    if (e == 0 && n > 0 && n <= few) count(n, p);
-    if (e == 0 && n > few) {
-      many_steps += paged_few_steps(a, n, p);
-      many_cost += paged_tc_user_cost(a, n, p);
+  int longest;  // pages of the longest unit, twice, and 1 if its user has several queries
+  int64_t mine, base, W;
+#pragma unroll 1
+  while (true) {
+    int64_t many_steps = 0, many_cost = 0;
+    int bad = 0;
+    mine = 0;
+    longest = 0;
+#pragma unroll 1
+    for (int u = u_lo; u < u_hi; ++u) {
+      int n, p;
+      const int e = kv_check_user(a.cu, a.past, u, a.U, a.T, a.max_pages, n, p);
+      bad |= e == 0 ? 0 : e == PTL_ERR_BAD_OFFSETS ? 1 : 2;
+      if (e != 0 || n == 0) continue;
+      if (n <= few) {
+        mine += paged_user_steps(a, n, p, few);
+        longest = max(longest, 2 * page_span(p + (n - 1) / PA_QG * PA_QG, p + n - 1, a.window, a.sinks).count + (n > 1));
+      } else {
+        many_steps += paged_few_steps(a, n, p);
+        many_cost += paged_tc_user_cost(a, n, p);
+      }
     }
-  }
-  if (__syncthreads_or(bad)) {  // every block sees the same offsets: nothing is written
-    const int offsets = __syncthreads_or(bad & 1);
-    pdl_wait();
-    if (blockIdx.x == 0 && tid == 0) set_error(a.err, offsets ? PTL_ERR_BAD_OFFSETS : PTL_ERR_BAD_PAGE);
-    return;
-  }
-  int64_t base, W;
-  auto scan = [&]() {
+    if (__syncthreads_or(bad)) {  // every block sees the same offsets: nothing is written
+      const int offsets = __syncthreads_or(bad & 1);
+      pdl_wait();
+      if (blockIdx.x == 0 && tid == 0) set_error(a.err, offsets ? PTL_ERR_BAD_OFFSETS : PTL_ERR_BAD_PAGE);
+      return;
+    }
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -203,45 +207,29 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS<SPLIT>) attn_paged_kerne
       if (lane >= o) incl += v;
     }
     longest = __reduce_max_sync(0xffffffffu, longest);
+    if (a.T > few) {
+      many_steps = warp_sum(many_steps);
+      many_cost = warp_sum(many_cost);
+    }
     if (lane == 31) {
       s_scan[warp] = incl;
       s_longest[warp] = longest;
+      s_many[0][warp] = many_steps;
+      s_many[1][warp] = many_cost;
     }
     __syncthreads();
     base = incl - mine;
-    W = 0;
+    W = many_steps = many_cost = 0;
 #pragma unroll
     for (int w = 0; w < H; ++w) {
       if (w < warp) base += s_scan[w];
       W += s_scan[w];
       longest = max(longest, s_longest[w]);
-    }
-  };
-  if (a.T > few) {  // (bf16) users with many new tokens: whose are they?
-    many_steps = warp_sum(many_steps);
-    many_cost = warp_sum(many_cost);
-    if (lane == 0) {
-      s_many[0][warp] = many_steps;
-      s_many[1][warp] = many_cost;
-    }
-  }
-  scan();
-  if (a.T > few) {
-    many_steps = many_cost = 0;
-#pragma unroll
-    for (int w = 0; w < H; ++w) {
       many_steps += s_many[0][w];
       many_cost += s_many[1][w];
     }
-    if (many_steps > 0 && paged_all_few(many_steps, many_cost)) {  // this kernel's: counted again
-      few = INT32_MAX;
-      for (int u = u_lo; u < u_hi; ++u) {
-        const int n = a.cu[u + 1] - a.cu[u];
-        if (n > a.few) count(n, a.past[u]);
-      }
-      __syncthreads();
-      scan();
-    }
+    if (many_steps == 0 || !paged_all_few(many_steps, many_cost)) break;
+    few = INT32_MAX;
   }
   // this block's steps [A, B), in so few blocks that no unit falls into too many
   int64_t G = W < int64_t(gridDim.x) ? W : int64_t(gridDim.x);
