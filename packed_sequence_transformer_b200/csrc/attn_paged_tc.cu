@@ -465,6 +465,11 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
         ifirst = p.first;
         ihead = p.head;
         ilist = a.table + p.list;
+        // the unit's queries into L2 while its first pages are on their way
+        const int row = 32 * cw + lane;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.qkv) + int64_t(p.row0 + row) * QKV_N + ihead * DH;
+        if (row < p.rows) prefetch_l2(q);
+        if (row + 128 < p.rows) prefetch_l2(q + 128 * QKV_N);
         ik += p.k0;
         iend = p.k0 + p.pages;
       }
@@ -523,9 +528,6 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
         const bool has = row < u.rows;
 #pragma unroll
         for (int c = 0; c < 8; ++c) x[c] = has ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        // into L2 meanwhile: the second tile's row, the next head's
-        if (i == 0 && row + 128 < u.rows) prefetch_l2(src + 128 * (QKV_N / 8));
-        if (has && u.head + 1 < H) prefetch_l2(src + 8);
         uint32_t mx = 0;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
