@@ -37,7 +37,7 @@
 // left out it is at most 7% shorter each, with all of the softmax left out 50%.
 // Measured: 16 users with 256 new tokens over 16,000: 244 us, 554 TFLOP/s; 100 of
 // each of 60 users over 2,000: 103 us; 31 users' prompts of 1,419 tokens (44,000
-// in all): 206 us; a call that only begins and ends, 25 us.
+// in all): 207 us; a call that only begins and ends, 25 us.
 //
 // Exponent: t = s q_row k_page + log2(v_page), w = 2^(t - m): the value scale,
 // a power of two, rides in the exponent, so that O accumulates over pages in
