@@ -31,7 +31,7 @@
 //
 // What bounds it: reading the pages, at 90 to 96% of the rate of a plain copy
 // when there are enough (250 users, one token each over 8,000: 2.05 GB in 333 to
-// 342 us); with a window of 1,000 the same users take 63 us (258 MB, 62%), the parts'
+// 342 us); with a window of 1,000 the same users take 61 us (258 MB, 65%), the parts'
 // beginnings and ends beside it; one user's token over 1,000: 11 us, two launches,
 // a page or two and one exchange of parts.  The fp32 build: 27 us for 5 new tokens
 // of 60 users over 700 (44 MB, 25%), its products twice as many on half the warps.
@@ -692,6 +692,17 @@ int launch_attn_paged(PagedArgs a, ptl_dtype dt, cudaStream_t st) {
   a.few = dt == PTL_BF16 ? PAGED_FEW : INT32_MAX;
   const int r = dt == PTL_BF16 ? launch_paged_t<__nv_bfloat16, 1>(a, st) : launch_paged_t<float, 2>(a, st);
   if (r != 0 || dt != PTL_BF16 || a.T <= PAGED_FEW) return r;
+  // A call too small for the other kernel, whatever its lengths are
+  // (paged_all_few): at most T / 33 users have more than PAGED_FEW = 32 new tokens
+  // and one unfinished group each, and no query sees more pages than the table or
+  // the window has.  The launch that finds nothing to do costs 3 us (60 users, one
+  // token each: 15 us with it, 12 without).
+  int64_t pages = a.max_pages;
+  if (a.window > 0) {
+    const int64_t seen = (a.window - 1) / KV_PAGE + 2 + (int64_t(a.sinks) + KV_PAGE - 1) / KV_PAGE;
+    if (seen < pages) pages = seen;
+  }
+  if (a.T <= PAGED_FEW_NEW && (a.T / 8 + a.T / (PAGED_FEW + 1) + 1) * pages < PAGED_FEW_STEPS) return r;
   return launch_attn_paged_tc(a, st);
 }
 

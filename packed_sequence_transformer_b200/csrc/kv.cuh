@@ -27,7 +27,7 @@ constexpr int KV_MIN_EXP = -100;            // smallest scale 2^-100
 // of 8), 33 take 99 in the second.  The fp32 build has the first kernel only:
 // fp16 operands hold no fp32 query in one part.
 constexpr int PAGED_FEW = 32;
-constexpr int PAGED_FEW_STEPS = 1000;
+constexpr int PAGED_FEW_STEPS = 1000, PAGED_FEW_NEW = 1024;
 constexpr int PAGED_TC_MAX_CTAS = 148;
 constexpr int PAGED_MAX_CTAS = 2 * 148;     // bound on the paged attention's grid (its workspace holds two parts per block)
 constexpr int KV_MAX_USERS = 1 << 30;       // a thread's range of users stays below 2^31
@@ -102,11 +102,11 @@ __device__ __forceinline__ int64_t paged_tc_user_cost(const PagedArgs& a, int n,
   return s;
 }
 // The same user's (8 queries, page) steps in the other kernel, about: as if all
-// groups saw what the middle one sees.  A user with more than 1,024 new tokens
+// groups saw what the middle one sees.  A user with more than PAGED_FEW_NEW new tokens
 // counts as too many for a whole call: one thread counts a user's groups one by
 // one (a sum over all users stays below 2^63).
 __device__ __forceinline__ int64_t paged_few_steps(const PagedArgs& a, int n, int past) {
-  if (n > 1024) return int64_t(1) << 40;
+  if (n > PAGED_FEW_NEW) return int64_t(1) << 40;
   const int mid = past + (n >> 1);
   return int64_t((n + 7) >> 3) * page_span(mid, mid, a.window, a.sinks).count;
 }
