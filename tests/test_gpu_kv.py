@@ -389,6 +389,39 @@ def test_same_bits_on_other_streams_and_in_graphs(dt, beside):
     assert ptl.last_device_error(wss[0]) == 0 and ptl.last_device_error(small) == 0
 
 
+@pytest.mark.parametrize("dt,beside", KINDS)
+def test_pages_beyond_32_bits_of_bytes(dt, beside):
+    """The same call at the far end of a cache of 4.6 GB: the same bits."""
+    total = 70000
+    c = Call(35, [3, 70, 1], [100, 700, 64], dt, beside=beside)
+    want = c.check().clone()
+    small = c.kv
+    kv = ptl.alloc_kv_pages(total)
+    kv.codes[total - c.num_pages:] = small.codes
+    kv.scales[total - c.num_pages:] = small.scales
+    table, c.kv = c.table_d, kv
+    c.table_d = torch.where(table < 0, table, table + (total - c.num_pages))
+    out, ws = c.attend()
+    torch.cuda.synchronize()
+    assert ptl.last_device_error(ws) == 0
+    assert torch.equal(out[:c.rows], want[:c.rows])
+    if beside:
+        return  # (its one page would be written many times at once)
+    assert ptl.last_device_error(c.append()) == 0
+    c.kv, far, c.table_d = small, kv, table
+    assert ptl.last_device_error(c.append()) == 0
+    assert torch.equal(far.codes[total - c.num_pages:], small.codes)
+    assert torch.equal(far.scales[total - c.num_pages:], small.scales)
+    assert not far.codes[:total - c.num_pages].any()
+    # and copied down
+    src = torch.arange(total - c.num_pages, total, dtype=torch.int32, device="cuda")
+    dst = src - 40000
+    ptl.kv_copy_pages(far, src, dst, ws)
+    torch.cuda.synchronize()
+    assert ptl.last_device_error(ws) == 0
+    assert torch.equal(far.codes[dst.long()], small.codes) and torch.equal(far.scales[dst.long()], small.scales)
+
+
 # ------------------------------------------------------------- page copy
 @pytest.mark.parametrize("pairs", [[(0, 1)], [(3, 0), (3, 5), (4, 1)], [(i, 39 - i) for i in range(20)]])
 def test_copy_pages(pairs):
