@@ -518,6 +518,11 @@ def _check_paged(qkv, cu_seqlens, kv: KvPages, page_table, past_lens, workspace,
     return T, users, max_pages
 
 
+def _check_window(window, sinks):
+    if not (-2 ** 31 <= window < 2 ** 31 and -2 ** 31 <= sinks < 2 ** 31):  # ctypes would cut them
+        raise ValueError("window and sinks must fit into 32 bits")
+
+
 def kv_append(qkv, cu_seqlens, kv: KvPages, page_table, past_lens, workspace, stream=None):
     """ptl_kv_append: the keys and values of qkv [T, 1536] into the pages, token
     i of user u at position past_lens[u] + i.  workspace: >= 256 bytes."""
@@ -541,6 +546,7 @@ def attention_paged(qkv, attn, cu_seqlens, kv: KvPages, page_table, past_lens, w
     """ptl_attention_paged: the new tokens' attention over the pages (which
     hold the new tokens too), causal, with window > 0 only the last `window`
     keys and the sequence's first `sinks`, into attn [T, 512]."""
+    _check_window(window, sinks)
     T, U, max_pages = _check_paged(qkv, cu_seqlens, kv, page_table, past_lens, workspace, attn)
     with _On(kv.index) as on:
         _check(lib().ptl_attention_paged(qkv.data_ptr(), attn.data_ptr(), cu_seqlens.data_ptr(), U, T, _dt(qkv.dtype),
@@ -607,6 +613,7 @@ class KvPool:
 
     def trim(self, seqs, window: int, sinks: int = 0) -> int:
         """Gives up the pages that no later token can see; how many became free."""
+        _check_window(window, sinks)
         s, sp, n = self._list(seqs)
         k = ctypes.c_int32()
         _check(lib().ptl_kv_pool_trim(self._p, sp, n, int(window), int(sinks), ctypes.byref(k)), "ptl_kv_pool_trim")

@@ -239,6 +239,13 @@ def test_binding_refuses(P):
         a = {**good, **over}
         with pytest.raises(ValueError):
             P.attention_paged(a["qkv"], a["attn"], a["cu"], kv, a["table"], a["past"], a["ws"], stream=0)
+    pool = P.KvPool(4, 2)
+    for window, sinks in [(2 ** 31, 0), (2 ** 32 + 5, 0), (-2 ** 31 - 1, 0), (5, 2 ** 31)]:
+        with pytest.raises(ValueError):
+            P.attention_paged(good["qkv"], good["attn"], good["cu"], kv, good["table"], good["past"], good["ws"],
+                              window, sinks, stream=0)
+        with pytest.raises(ValueError):
+            pool.trim([0], window, sinks)
     with pytest.raises(ValueError):
         P.kv_copy_pages(kv, torch.zeros(2, **i32), torch.zeros(3, **i32), good["ws"], stream=0)
     with pytest.raises(ValueError):
