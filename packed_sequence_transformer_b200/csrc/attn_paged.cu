@@ -31,7 +31,7 @@
 //
 // What bounds it: reading the pages, at 90 to 96% of the rate of a plain copy
 // when there are enough (250 users, one token each over 8,000: 2.05 GB in 333 to
-// 342 us); with a window of 1,000 the same users take 61 us (258 MB, 65%), the parts'
+// 346 us); with a window of 1,000 the same users take 61 us (258 MB, 65%), the parts'
 // beginnings and ends beside it; one user's token over 1,000: 11 us, two launches,
 // a page or two and one exchange of parts.  The fp32 build: 27 us for 5 new tokens
 // of 60 users over 700 (44 MB, 25%), its products twice as many on half the warps.
