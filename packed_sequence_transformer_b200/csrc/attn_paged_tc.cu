@@ -41,12 +41,15 @@
 //
 // Exponent: t = s q_row k_page + log2(v_page), w = 2^(t - m): the value scale,
 // a power of two, rides in the exponent, so that O accumulates over pages in
-// TMEM; the normaliser adds w / v_page.  m comes from the maximum of the pages
-// before; only when a page exceeds that by 2^4 is m raised and O rescaled in
-// place.  A page of small values (v_page far below the others') may weigh
-// nothing in O and all in the normaliser: where its w would fall below what fp32
-// holds, they are taken relative to the page's own maximum and the normaliser's
-// part is scaled instead; factors of a normaliser are applied in two halves.
+// TMEM.  m comes from the maximum of the pages before; only when a page exceeds
+// that by 2^4 is m raised and O rescaled in place.  The normaliser counts scores
+// without value scales: l = sum 2^(s - n) has a reference n of its own, the
+// largest score (raised like m), so that l lies between about 1 and 2^4 times the
+// number of keys whatever the scales are (relative to m, 131 pages of zero values
+// took it beyond fp32).  A page adds its w times 2^(m - log2(v_page) - n); where
+// its w would fall below what fp32 holds, which weighs nothing in O but may weigh
+// all in l, they are taken relative to the page's own maximum.  At last
+// out = O / l 2^(m - n).
 // Values that are NaN codes in a page that some query does not see wholly are
 // taken out by the converters and given back, per row, to the queries that see
 // them.  Every wait is bounded.
@@ -82,12 +85,15 @@ constexpr int PTC_STAGE = 2 * PTC_OPERAND;
 constexpr int PTC_QTILE = 128 * 128;
 constexpr int PTC_RAW_BYTES = 2 * KV_TILE;
 constexpr int PTC_SMEM = 4 * PTC_QTILE + PTC_STAGES * PTC_STAGE + 2 * PTC_RAW * PTC_RAW_BYTES + 1024;
-constexpr int PTC_PART = 128 * (DH + 2);  // floats of one tile's part
+constexpr int PTC_PART = 128 * (DH + 4);  // floats of one tile's part: O, then (m, n, l, 0) per row
 // A tile's reference m lies 2^PTC_TOP below the largest exponent it was taken
 // from, and is taken anew when a page exceeds that by 2^PTC_RAISE: weights reach
 // 2^15 at most, and fp16 holds them to 2^-35 of the largest (with weights of 1
 // for the largest, what lay 2^-25 below it was lost, as much as 2^20 tokens of it).
 constexpr float PTC_TOP = 11.f, PTC_RAISE = 4.f;
+// n, and the m of several groups, of a row that has seen nothing: below any score, and differences of two are
+// numbers (a test for -inf at each of them cost 5% of a call's time).
+constexpr float PTC_NONE = -3e38f;
 
 __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
@@ -148,11 +154,6 @@ __device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     if ((i & 63) == 0 && __any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs)) return false;
   }
-}
-// l 2^d, where 2^d alone may be below the smallest number
-__device__ __forceinline__ float scale_sum(float l, float d) {
-  const float e = ex2_approx(0.5f * d);
-  return l * e * e;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -272,16 +273,17 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
   // so that each waits for every phase of the one that it looks at)
   __shared__ uint64_t x_full[2][PTC_GROUPS], x_empty[PTC_GROUPS], group_bar[PTC_GROUPS];
   __shared__ float s_rawscale[2][PTC_RAW][2];
-  // [stage] key scale, value scale's log2 and reciprocal, page number * 4 with
-  // bits 0 and 1: tile 0's and 1's queries all see all of it
+  // [stage] key scale, value scale's log2, page number * 4 with bits 0 and 1:
+  // tile 0's and 1's queries all see all of it
   __shared__ __align__(16) float4 s_meta[PTC_STAGES];
   __shared__ __align__(8) uint2 s_hasnan[PTC_STAGES];      // [stage] each warp of the pair took out NaN values
   __shared__ __align__(8) uint16_t s_nan[PTC_STAGES][64][4];  // which tokens of row d
   __shared__ int s_stage[PTC_GROUPS];                      // the stage of the group's page
   __shared__ float s_c[2][PTC_QB];                         // [slot][row] exponent's factor
-  __shared__ float s_xm[PTC_GROUPS][128], s_xl[PTC_GROUPS][128];  // maxima and sums handed over
+  __shared__ float s_xm[PTC_GROUPS][128], s_xn[PTC_GROUPS][128], s_xl[PTC_GROUPS][128];  // m, n, l handed over
   __shared__ uint64_t s_xnan[PTC_GROUPS][128];
-  __shared__ float s_wm[PTC_GROUPS][128], s_wl[PTC_GROUPS][128];  // of the rows whose parts are added
+  __shared__ float s_wm[PTC_GROUPS][128];   // of the rows whose parts are added: m, and 1 / l, 2^(m - n)
+  __shared__ float2 s_wl[PTC_GROUPS][128];
   __shared__ int64_t s_scan[PTC_THREADS / 32], s_few[PTC_THREADS / 32];
   __shared__ int64_t s_start;
   __shared__ int s_first[3];
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
         const int whole = int(u.tile[0].whole(page)) | int(u.tile[1].whole(page)) << 1;
         if (ct == 0) {
           const float ks = s_rawscale[pair][raw_c][0], vs = s_rawscale[pair][raw_c][1];
-          s_meta[st] = make_float4(ks, __log2f(vs), __fdividef(1.0f, vs), __int_as_float(page << 2 | whole));
+          s_meta[st] = make_float4(ks, __log2f(vs), __int_as_float(page << 2 | whole), 0.f);
         }
         bool nan_any = false;
         if (whole != 3) {
@@ -734,7 +736,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
       const float c = s_c[slot][128 * tile + r];
       mbar_arrive(&q_empty[slot]);
       singles += !two;
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, nm = PTC_NONE, l = 0.f;
       uint64_t nans = 0;  // dims of this row that saw a NaN value
 #pragma unroll 1
       for (int i = 0; i < pages; ++i) {
@@ -749,7 +751,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
         // the exponent's factor and offset; the factor not below the smallest
         // normal number: a masked -inf times 0 would be NaN
         const float ck = fmaxf(c * mt.x, 1.17549435e-38f);
-        const int pw = __float_as_int(mt.w);
+        const int pw = __float_as_int(mt.z);
         const bool whole = (pw >> tile) & 1;
         uint64_t see = ~0ull;
         if (!whole) see = page_visible(p0r, (pw >> 2) * KV_PAGE, a.window, a.sinks);
@@ -769,7 +771,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
           for (int e = 0; e < 32; e += 2)
             mx[(e >> 1) & 1] = fmax3(mx[(e >> 1) & 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
         }
-        const float top = fmaf(fmaxf(mx[0], mx[1]), ck, mt.y);
+        const float score = fmaxf(mx[0], mx[1]) * ck, top = score + mt.y;
         if (i == 0) {
           m = top - PTC_TOP;
         } else if (__any_sync(0xffffffffu, top > m + (PTC_TOP + PTC_RAISE))) {
@@ -784,14 +786,11 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
             tmem_st16(tO + 16 * h, o);
           }
-          l = scale_sum(l, d);
           m = mn;
         }
-        float off = mt.y - (m == -INFINITY ? 0.f : m), part = mt.z;
-        if (top < m - 64.f && top != -INFINITY) {  // nothing in O: weights of 2^-26 and less, which are 0 in fp16
+        float off = mt.y - (m == -INFINITY ? 0.f : m);
+        if (top < m - 64.f && top != -INFINITY)  // nothing in O: weights of 2^-26 and less, which are 0 in fp16
           off = mt.y - top - 26.f;
-          part = ex2_approx(top - m + 26.f - mt.y);
-        }
         const uint64_t ck2 = f2_pack(ck, ck), off2 = f2_pack(off, off);
         uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll 1
@@ -818,10 +817,6 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
           }
           tmem_st16(tS + 16 * h, pk);  // over scores that have been read
         }
-        float a0, a1, a2, a3;
-        f2_unpack(sum[0], a0, a1);
-        f2_unpack(sum[1], a2, a3);
-        l = fmaf((a0 + a1) + (a2 + a3), part, l);
         const uint2 has = s_hasnan[st];
         if (has.x | has.y) {
 #pragma unroll 1
@@ -831,6 +826,17 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&p_full[g]);
+        // The normaliser, beside the page's product.  (The factor is at most 2^69
+        // where the row sees a key of the page; the bound is for the others, whose
+        // weights are 0.)
+        if (score > nm + PTC_RAISE) {
+          l *= ex2_approx(nm - score);
+          nm = score;
+        }
+        float a0, a1, a2, a3;
+        f2_unpack(sum[0], a0, a1);
+        f2_unpack(sum[1], a2, a3);
+        l = fmaf((a0 + a1) + (a2 + a3), ex2_approx(fminf(-off - nm, 80.f)), l);
       }
       if (!ok) break;
 
@@ -852,6 +858,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
           break;
         }
         s_xm[g][r] = m;
+        s_xn[g][r] = nm;
         s_xl[g][r] = pages > 0 ? l : -1.f;  // -1: no page, no O
         s_xnan[g][r] = nans;
         tc_fence_before();
@@ -861,7 +868,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
       const int donors = two ? 1 : 3, row_base = u.row0 + 128 * tile, c0 = u.c0, c1 = u.c1;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + int64_t(row_base) * D + u.head * DH;
       mbar_arrive(&u_empty[us]);
-      float M = m;
+      float M = fmaxf(m, PTC_NONE), N = nm;
 #pragma unroll 1
       for (int d = 1; d <= donors; ++d) {
         if (!warp_wait_bar(&x_full[two][g + d], (two ? unit - singles : singles - 1) & 1)) {
@@ -869,25 +876,27 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
           break;
         }
         M = fmaxf(M, s_xm[g + d][r]);
+        N = fmaxf(N, s_xn[g + d][r]);
       }
       if (!ok) break;
       tc_fence_after();
       // each group's weight takes the place of its maximum
-      s_xm[g][r] = pages > 0 && M != -INFINITY ? ex2_approx(m - M) : 0.f;
+      s_xm[g][r] = ex2_approx(m - M);
       s_xl[g][r] = pages > 0 ? l : -1.f;
-      l = M == -INFINITY ? 0.f : scale_sum(l, m - M);
+      l *= ex2_approx(nm - N);
 #pragma unroll 1
       for (int d = 1; d <= donors; ++d) {
-        const float ld = s_xl[g + d][r], below = M == -INFINITY ? -INFINITY : s_xm[g + d][r] - M;
-        s_xm[g + d][r] = ex2_approx(below);
-        if (ld != -1.f) l += scale_sum(ld, below);
+        const float ld = s_xl[g + d][r];
+        s_xm[g + d][r] = ex2_approx(s_xm[g + d][r] - M);
+        if (ld != -1.f) l = fmaf(ld, ex2_approx(s_xn[g + d][r] - N), l);
         nans |= s_xnan[g + d][r];
       }
-      m = M;
       if (c0 != c1) pdl_wait();  // the counters are zero, the parts' room is free
       auto part = [&](int i) { return a.partial + (int64_t(2 * i + (i == c0 ? 1 : 0)) * 2 + tile) * PTC_PART; };
       float* mp = part(blockIdx.x);
-      const float inv = 1.0f / l;
+      // (two factors: 2^(M - N) is as small as 2^-115 where all values are, and
+      // l may be large besides)
+      const float inv = 1.0f / l, by = ex2_approx(M - N);
 #pragma unroll 1
       for (int h = 0; h < 4; ++h) {  // 16 dims at a time
         float o[16];
@@ -911,11 +920,11 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
           if (c0 == c1) {
             uint4* dst = reinterpret_cast<uint4*>(out + int64_t(r) * D + 16 * h);
 #pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = o[e] * inv * by;
+#pragma unroll
             for (int k = 0; k < 2; ++k)
-              dst[k] = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
-                                  pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                                  pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                                  pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+              dst[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                                  pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
           } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -932,7 +941,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
         mbar_arrive(&x_empty[g + d]);
       }
       if (c0 == c1) continue;
-      if (r < rows) __stcg(reinterpret_cast<float2*>(mp + 128 * DH + 2 * r), make_float2(m, l));
+      if (r < rows) __stcg(reinterpret_cast<float4*>(mp + 128 * DH) + r, make_float4(M, N, l, 0.f));
       __threadfence();
       if (!meet()) break;
       if (r == 0) s_done[g] = atomicAdd(a.counters + PAGED_MAX_CTAS * H + 2 * c0 + tile, 1);
@@ -941,20 +950,20 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
       // The last part: add them up, in block order.  Thread r finds row r's
       // maximum and sum, then holds 4 dims of each 8th row.
       __threadfence();
-      M = -INFINITY;
+      M = N = PTC_NONE;
       float L = 0.f;
       if (r < rows) {
 #pragma unroll 4
         for (int i = c0; i <= c1; ++i) {
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(i) + 128 * DH + 2 * r));
-          const float mn = fmaxf(M, ml.x), ref = mn == -INFINITY ? 0.f : mn;
-          L = scale_sum(L, M - ref) + scale_sum(ml.y, ml.x - ref);
-          M = mn;
+          const float4 p = __ldcg(reinterpret_cast<const float4*>(part(i) + 128 * DH) + r);
+          const float nn = fmaxf(N, p.y);
+          L = L * ex2_approx(N - nn) + p.z * ex2_approx(p.y - nn);
+          N = nn;
+          M = fmaxf(M, p.x);
         }
-        if (M == -INFINITY) M = 0.f;
       }
       s_wm[g][r] = M;
-      s_wl[g][r] = 1.0f / L;
+      s_wl[g][r] = make_float2(1.0f / L, ex2_approx(M - N));
       if (!meet()) break;
 #pragma unroll 1
       for (int h = 0; h < 4; ++h) {  // 32 rows at a time
@@ -969,7 +978,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
           for (int j = 0; j < 4; ++j) {
             const int row = first + 8 * j;
             if (row >= rows) continue;
-            const float we = ex2_approx(__ldcg(pi + 128 * DH + 2 * row) - s_wm[g][row]);
+            const float we = ex2_approx(__ldcg(pi + 128 * DH + 4 * row) - s_wm[g][row]);
             const float4 v = __ldcg(reinterpret_cast<const float4*>(pi + row * DH) + (r & 15));
             acc[j].x = fmaf(we, v.x, acc[j].x);
             acc[j].y = fmaf(we, v.y, acc[j].y);
@@ -981,9 +990,10 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
         for (int j = 0; j < 4; ++j) {
           const int row = first + 8 * j;
           if (row >= rows) continue;
-          const float iv = s_wl[g][row];
+          const float2 f = s_wl[g][row];
           *reinterpret_cast<uint2*>(out + int64_t(row) * D + 4 * (r & 15)) =
-              make_uint2(pack_bf16x2(acc[j].x * iv, acc[j].y * iv), pack_bf16x2(acc[j].z * iv, acc[j].w * iv));
+              make_uint2(pack_bf16x2(acc[j].x * f.x * f.y, acc[j].y * f.x * f.y),
+                         pack_bf16x2(acc[j].z * f.x * f.y, acc[j].w * f.x * f.y));
         }
       }
       if (!meet()) break;  // before another unit's rows take the places of these
