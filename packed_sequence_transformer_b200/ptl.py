@@ -224,8 +224,8 @@ def _stream(stream) -> ctypes.c_void_p:
 
 class _On:
     """The device of a call's tensors as the current one, and the stream to use
-    there: the caller's, or that device's current stream.  CPU tensors leave
-    both as they are (the library then refuses or returns without work).  A
+    there: the caller's, or that device's current stream.  CPU tensors, which
+    only a call without work may have, leave both as they are.  A
     call on the paged cache may be one small kernel, so this is written to
     cost less than launching it: torch's device guard and stream objects are
     made only where they are needed."""
@@ -483,7 +483,7 @@ class KvPages:
         self.codes, self.scales = codes, scales
         self._struct = KvPagesStruct(_ptr(codes), _ptr(scales), n)
         self._ref = ctypes.byref(self._struct)
-        self.index = codes.get_device()  # -1: CPU tensors, which the library refuses
+        self.index = codes.get_device()  # -1: CPU tensors, which every call with work to do refuses
 
 
 def alloc_kv_pages(num_pages: int, device="cuda") -> KvPages:
@@ -515,6 +515,8 @@ def _check_paged(qkv, cu_seqlens, kv: KvPages, page_table, past_lens, workspace,
             raise ValueError("tensors passed to libptl must be contiguous")
         if t.get_device() != index:  # (-1: a CPU tensor)
             raise ValueError("all tensors of a call must be on one device")
+    if index < 0 and T > 0:  # the library would hand their addresses to a kernel
+        raise ValueError("the tensors of a call must be on a GPU")
     return T, users, max_pages
 
 
@@ -565,6 +567,8 @@ def kv_copy_pages(kv: KvPages, src, dst, workspace, stream=None):
         raise ValueError("tensors passed to libptl must be contiguous")
     if any(t.get_device() != kv.index for t in (src, dst, workspace)):
         raise ValueError("all tensors of a call must be on one device")
+    if kv.index < 0 and src.numel() > 0:
+        raise ValueError("the tensors of a call must be on a GPU")
     with _On(kv.index) as on:
         _check(lib().ptl_kv_copy_pages(kv._ref, src.data_ptr(), dst.data_ptr(), src.numel(), workspace.data_ptr(),
                                        workspace.numel() * workspace.element_size(), on.stream(stream)),

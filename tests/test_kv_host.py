@@ -297,3 +297,24 @@ def test_oracle_attention_against_dense():
         p = np.exp(s - s.max(-1, keepdims=True))
         want = np.einsum("htj,jhd->thd", p / p.sum(-1, keepdims=True), v)
         np.testing.assert_allclose(got, want, rtol=0, atol=1e-12)
+
+
+def test_binding_refuses_cpu_tensors(P, monkeypatch):
+    """Before any library call: with a GPU in the machine the library would
+    launch kernels on their addresses."""
+    kv = P.KvPages(torch.zeros(3, 2, 8, 64, 64, dtype=torch.uint8), torch.ones(3, 2, 8))
+    i32 = dict(dtype=torch.int32)
+    cu, table, past = torch.tensor([0, 5], **i32), torch.zeros(1, 2, **i32), torch.zeros(1, **i32)
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+
+    def reached():
+        raise AssertionError("the library was called")
+
+    monkeypatch.setattr(P, "lib", reached)
+    for stream in (None, 0):
+        with pytest.raises(ValueError):
+            P.kv_append(torch.zeros(5, 1536), cu, kv, table, past, ws, stream=stream)
+        with pytest.raises(ValueError):
+            P.attention_paged(torch.zeros(5, 1536), torch.zeros(5, 512), cu, kv, table, past, ws, stream=stream)
+        with pytest.raises(ValueError):
+            P.kv_copy_pages(kv, torch.zeros(2, **i32), torch.ones(2, **i32), ws, stream=stream)
