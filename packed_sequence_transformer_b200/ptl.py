@@ -10,6 +10,7 @@ raises; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import Dict, Iterable, List, Optional
 
@@ -493,6 +494,15 @@ def alloc_kv_pages(num_pages: int, device="cuda") -> KvPages:
 
 
 _I32 = torch.int32
+_INTEGERS = (torch.int32, torch.int64, torch.int16, torch.int8, torch.uint8)
+
+
+def _int32(value) -> int:
+    """An integer for a 32-bit argument (ctypes would cut it)."""
+    value = operator.index(value)
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError("numbers passed to libptl must fit into 32 bits")
+    return value
 
 
 def _check_paged(qkv, cu_seqlens, kv: KvPages, page_table, past_lens, workspace, attn=None):
@@ -537,7 +547,7 @@ def kv_append(qkv, cu_seqlens, kv: KvPages, page_table, past_lens, workspace, st
 
 
 def attention_paged_workspace(max_tokens: int, max_users: int, dtype, device="cuda") -> torch.Tensor:
-    n = int(lib().ptl_attention_paged_workspace_size(int(max_tokens), int(max_users), _dt(dtype)))
+    n = int(lib().ptl_attention_paged_workspace_size(_int32(max_tokens), _int32(max_users), _dt(dtype)))
     if n == 0:
         raise ValueError("invalid workspace request")
     return torch.zeros(n, dtype=torch.uint8, device=device)
@@ -582,14 +592,22 @@ class KvPool:
     its own ``KvPages``.  Lists come back as int32 CPU tensors."""
 
     def __init__(self, num_pages: int, num_seqs: int):
+        num_pages, num_seqs = _int32(num_pages), _int32(num_seqs)
         p = ctypes.c_void_p()
-        _check(lib().ptl_kv_pool_create(int(num_pages), int(num_seqs), ctypes.byref(p)), "ptl_kv_pool_create")
+        _check(lib().ptl_kv_pool_create(num_pages, num_seqs, ctypes.byref(p)), "ptl_kv_pool_create")
         self._p = p
         self.num_pages, self.num_seqs = num_pages, num_seqs
 
     @staticmethod
     def _list(values):
-        t = torch.as_tensor(values, dtype=torch.int32, device="cpu").reshape(-1).contiguous()
+        try:
+            t = torch.as_tensor(values, device="cpu").reshape(-1)
+        except (RuntimeError, OverflowError) as e:
+            raise ValueError("sequences and lengths must be integers of 32 bits") from e
+        if t.dtype is not _I32 and t.numel() > 0 and (t.dtype not in _INTEGERS or int(t.min()) < -2 ** 31
+                                                      or int(t.max()) >= 2 ** 31):
+            raise ValueError("sequences and lengths must be integers of 32 bits")
+        t = t.to(_I32).contiguous()
         return t, ctypes.cast(t.data_ptr(), _I32P), t.numel()
 
     def reserve(self, seqs, new_lens) -> None:
@@ -620,7 +638,7 @@ class KvPool:
         _check_window(window, sinks)
         s, sp, n = self._list(seqs)
         k = ctypes.c_int32()
-        _check(lib().ptl_kv_pool_trim(self._p, sp, n, int(window), int(sinks), ctypes.byref(k)), "ptl_kv_pool_trim")
+        _check(lib().ptl_kv_pool_trim(self._p, sp, n, _int32(window), _int32(sinks), ctypes.byref(k)), "ptl_kv_pool_trim")
         return k.value
 
     def compact(self):
@@ -640,13 +658,14 @@ class KvPool:
         s, sp, n = self._list(seqs)
         if max_pages is None:
             max_pages = max([1] + [-(-self.length(q) // KV_PAGE) for q in s.tolist()])
+        max_pages = _int32(max_pages)
         t = torch.empty(n, max_pages, dtype=torch.int32)
-        _check(lib().ptl_kv_pool_table(self._p, sp, n, int(max_pages), ctypes.cast(t.data_ptr(), _I32P)),
+        _check(lib().ptl_kv_pool_table(self._p, sp, n, max_pages, ctypes.cast(t.data_ptr(), _I32P)),
                "ptl_kv_pool_table")
         return t
 
     def length(self, seq: int) -> int:
-        return int(lib().ptl_kv_pool_length(self._p, int(seq)))
+        return int(lib().ptl_kv_pool_length(self._p, _int32(seq)))
 
     @property
     def free_pages(self) -> int:

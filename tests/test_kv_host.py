@@ -318,3 +318,33 @@ def test_binding_refuses_cpu_tensors(P, monkeypatch):
             P.attention_paged(torch.zeros(5, 1536), torch.zeros(5, 512), cu, kv, table, past, ws, stream=stream)
         with pytest.raises(ValueError):
             P.kv_copy_pages(kv, torch.zeros(2, **i32), torch.ones(2, **i32), ws, stream=stream)
+
+
+def test_pool_numbers_are_not_cut(P):
+    """Numbers that do not fit into 32 bits, or are no integers, are refused; none
+    is taken for another."""
+    pool = P.KvPool(4, 3)
+    pool.reserve([0, 1], [100, 3])
+    before = pool.table(range(3), 4).tolist(), pool.free_pages
+    far = 2 ** 32
+    for one in ([far], [far + 1], [-far], [2 ** 31], [2 ** 63], [2 ** 70], [0.0], [0.5], [True], torch.tensor([far]),
+                np.array([far + 2]), np.array([2 ** 64 - far], np.uint64), torch.tensor([1.0]), torch.tensor([0.0, 1.0])):
+        for call in (lambda x: pool.release(x), lambda x: pool.trim(x, 5), lambda x: pool.table(x, 4),
+                     lambda x: pool.reserve(x, [101]), lambda x: pool.fork(x, [2]), lambda x: pool.fork([0], x)):
+            with pytest.raises(ValueError):
+                call(one)
+    for length in ([far + 101], torch.tensor([far + 101]), [101.5]):
+        with pytest.raises(ValueError):
+            pool.reserve([0], length)
+    for call in (lambda: pool.length(far), lambda: pool.table([0], far + 2), lambda: pool.trim([0], 1.5),
+                 lambda: P.KvPool(far + 1, 1), lambda: P.KvPool(1, far + 1), lambda: P.KvPool(1.5, 1),
+                 lambda: P.attention_paged_workspace(1, far + 1, "bf16", device="cpu")):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+    assert (pool.table(range(3), 4).tolist(), pool.free_pages) == before
+    # what fits is taken in any integer type
+    for seqs in (torch.tensor([0, 1]), np.array([0, 1], np.int64), np.array([0, 1], np.uint8), (0, 1), range(2),
+                 [np.int64(0), 1], torch.tensor([0, 1], dtype=torch.int32)):
+        assert pool.table(seqs, 4).tolist() == before[0][:2]
+    pool.release([])
+    assert pool.table([], 2).shape == (0, 2)
