@@ -512,6 +512,8 @@ def _check_paged(qkv, cu_seqlens, kv: KvPages, page_table, past_lens, workspace,
     users, max_pages = page_table.shape
     if width != 1536:
         raise ValueError("qkv must be [T, 1536]")
+    if users >= 2 ** 31 or max_pages >= 2 ** 31:  # ctypes would cut them
+        raise ValueError("the page table's rows and columns must fit into 32 bits")
     if past_lens.shape != (users,) or cu_seqlens.shape != (users + 1,):
         raise ValueError("cu_seqlens [U + 1], page_table [U, max_pages] and past_lens [U] do not agree")
     if cu_seqlens.dtype is not _I32 or page_table.dtype is not _I32 or past_lens.dtype is not _I32:

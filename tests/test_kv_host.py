@@ -348,3 +348,17 @@ def test_pool_numbers_are_not_cut(P):
         assert pool.table(seqs, 4).tolist() == before[0][:2]
     pool.release([])
     assert pool.table([], 2).shape == (0, 2)
+
+
+def test_wide_page_tables_are_not_cut(P):
+    kv = P.KvPages(torch.zeros(3, 2, 8, 64, 64, dtype=torch.uint8), torch.ones(3, 2, 8))
+    i32 = dict(dtype=torch.int32)
+    qkv, out, ws = torch.zeros(5, 1536), torch.zeros(5, 512), torch.zeros(1 << 16, dtype=torch.uint8)
+    meta = dict(dtype=torch.int32, device="meta")
+    for cu, table, past in [(torch.zeros(2, **i32), torch.empty(1, 2 ** 32 + 1, **meta), torch.zeros(1, **i32)),
+                            (torch.empty(2 ** 32 + 2, **meta), torch.empty(2 ** 32 + 1, 1, **meta),
+                             torch.empty(2 ** 32 + 1, **meta))]:
+        with pytest.raises(ValueError, match="32 bits"):
+            P.attention_paged(qkv, out, cu, kv, table, past, ws, stream=0)
+        with pytest.raises(ValueError, match="32 bits"):
+            P.kv_append(qkv, cu, kv, table, past, ws, stream=0)
