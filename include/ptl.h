@@ -456,7 +456,8 @@ ptl_status ptl_partition_users(const int32_t* cu_seqlens, int32_t num_users, int
 /* ---- The 8-bit paged key/value cache. ----
  * A served user's history need not be computed again for each request: its
  * keys and values are kept in pages, quantised to e4m3, and only the new
- * tokens (the next action, or the candidates to score) run through the layer.
+ * tokens (the next actions, or candidates to score: see ptl_attention_paged on
+ * what those see) run through the layer.
  * One layer of a served batch is then ptl_qkv_projection, ptl_kv_append,
  * ptl_attention_paged, ptl_out_projection, ptl_gate, ptl_moe, with one
  * ptl_kv_pages per layer and one page table for all layers.
@@ -482,8 +483,12 @@ ptl_status ptl_partition_users(const int32_t* cu_seqlens, int32_t num_users, int
  * nothing but bits that fall below e4m3's smallest step.  Infinities and NaN
  * are stored as NaN and do not count for the scale.  A page whose first token
  * is new is written whole, zeros behind the tokens; elsewhere bytes behind the
- * last token stay as they are.  Positions may be written again (tokens taken
- * back, then others appended).  A page must not be written for two users in
+ * last token stay as they are.  Positions may be written again (a smaller
+ * past_lens[u]: tokens taken back, then others appended), but what was appended
+ * leaves its mark: a scale that it raised stays raised while the page keeps
+ * tokens, and their codes stay rounded at it.  Where the history has to stay as it
+ * was, append to a fork of it (ptl_kv_pool_fork) and release that; the pool itself
+ * does not take tokens back.  A page must not be written for two users in
  * one call, and not while another sequence shares it: its contents are then
  * undefined.  workspace: at least 256 bytes (the error word).
  *
@@ -495,8 +500,18 @@ ptl_status ptl_partition_users(const int32_t* cu_seqlens, int32_t num_users, int
  * window <= 0: no window, sinks unused.  Only the pages that some query sees
  * are read; what masked positions hold, NaN included, has no effect.  Two
  * users of a call may name the same pages.  attn: [T][512] in dt.
- * PTL_ERR_BAD_MASK for sinks < 0.  workspace:
- * ptl_attention_paged_workspace_size(T, U, dt) bytes.
+ * The new tokens of a user follow one another, so each sees those before it:
+ * candidates appended together would see one another, which they do not in
+ * ptl_attention_masked.  To score them apart, make a fork of the history for each
+ * group (one page copied, the others shared), append and attend for the forks as
+ * users of one call, and release them.
+ * Sums are held in fp32, relative to the largest weight of a row; the weights of
+ * the values are rounded to fp16 in the bf16 build (to two halves, 22 bits, in the
+ * fp32 build).  The sum of |value| over the keys that a query sees must stay below
+ * 2^127.  PTL_ERR_BAD_MASK for sinks < 0.  workspace:
+ * ptl_attention_paged_workspace_size(T, U, dt) bytes (21 MB, whatever T, U and dt
+ * are).  The error word is that of the last call with this workspace: append and
+ * attention need one each where both are to be read at the end.
  *
  * Device checks of both: cu_seqlens as everywhere; past_lens[u] < 0 or
  * past_lens[u] + n > 64 max_pages set PTL_ERR_BAD_PAGE, and in either case

@@ -564,3 +564,72 @@ def test_layer_over_the_cache(dt):
                 table[users].contiguous(), dev(np.array([case.lengths[u] - 1 for u in users]), torch.int32))
     b = c.bound(ref, mag, smax, count)[rows]
     assert (np.abs(host(one[1]).reshape(3, 8, 64) - ref[rows]) <= b).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_candidates_as_forks(dt):
+    """Groups of candidates that do not see one another, as ptl_attention_masked
+    has them, over the cache: a fork of the history for each group.  Against the
+    masked oracle on what the pages hold; the histories' pages stay as they were."""
+    rng = np.random.default_rng(41)
+    lens, groups, size = [200, 75], 3, 2
+    pool, kv = ptl.KvPool(24, 8), ptl.alloc_kv_pages(24)
+    ws = ptl.attention_paged_workspace(300, 8, dt)
+
+    def call(seqs, past, qkv, attend):
+        new = [pool.length(s) - p for s, p in zip(seqs, past)]
+        cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        args = (dev(cu, torch.int32), kv, pool.table(seqs).cuda(), dev(np.array(past), torch.int32), ws)
+        ptl.kv_append(qkv, *args)
+        torch.cuda.synchronize()
+        assert ptl.last_device_error(ws) == 0
+        if not attend:
+            return None
+        out = torch.empty(len(qkv), 512, dtype=tdt(dt), device="cuda")
+        ptl.attention_paged(qkv, out, *args)
+        torch.cuda.synchronize()
+        assert ptl.last_device_error(ws) == 0
+        return cu, out
+
+    pool.reserve([0, 1], lens)
+    hist = rng.standard_normal((sum(lens), 1536)).astype(np.float32)
+    for first in (0, lens[0]):  # no candidate raises a page's scale: the forks hold the same history
+        hist[first:first + (lens[0] if first == 0 else lens[1]):64, 512:] = 8.0
+    call([0, 1], [0, 0], dev(hist, tdt(dt)), False)
+    codes, scales, free = kv.codes.clone(), kv.scales.clone(), pool.free_pages
+    held = pool.table([0, 1], 4)[pool.table([0, 1], 4) >= 0].long()
+
+    forks, src = list(range(2, 2 + 2 * groups)), [0] * groups + [1] * groups
+    ptl.kv_copy_pages(kv, *(x.cuda() for x in pool.fork(src, forks)), ws)
+    past = [lens[s] for s in src]
+    pool.reserve(forks, [p + size for p in past])
+    cand = dev(rng.standard_normal((2 * groups * size, 1536)).astype(np.float32).clip(-4, 4), tdt(dt))
+    cu, out = call(forks, past, cand, True)
+    assert torch.equal(kv.codes[held.cuda()], codes[held.cuda()])
+    assert torch.equal(kv.scales[held.cuda()], scales[held.cuda()])
+
+    vals, sc, table = value_of_codes(kv.codes), host(kv.scales), pool.table(forks).numpy()
+    q = host(cand)[:, :512].reshape(-1, 8, 64)
+    seqs = [O.paged_sequence(vals, sc, [p for p in t if p >= 0], p0 + size) for t, p0 in zip(table, past)]
+    keys, values, queries, at = [], [], [], []
+    for u in range(2):
+        mine = range(u * groups, (u + 1) * groups)
+        n = lens[u]
+        for f in mine:
+            assert np.array_equal(seqs[f][0][:n], seqs[u * groups][0][:n])
+            assert np.array_equal(seqs[f][1][:n], seqs[u * groups][1][:n])
+        keys += [seqs[u * groups][0][:n]] + [seqs[f][0][n:] for f in mine]
+        values += [seqs[u * groups][1][:n]] + [seqs[f][1][n:] for f in mine]
+        at += list(range(sum(map(len, queries)) + n, sum(map(len, queries)) + n + groups * size))
+        queries += [np.zeros((n, 8, 64)), q[u * groups * size:(u + 1) * groups * size]]
+    total = [n + groups * size for n in lens]
+    want = O.jagged_hstu_attention(np.concatenate(queries), np.concatenate(keys), np.concatenate(values),
+                                   np.concatenate([[0], np.cumsum(total)]), num_targets=[groups * size] * 2,
+                                   target_group_size=size)[at]
+    ref, mag, smax, count = O.attention_paged(q, vals, sc, cu, table, past, details=True)
+    np.testing.assert_allclose(ref, want, rtol=0, atol=1e-12)
+    c = Call.__new__(Call)
+    c.dt, c.kv = dt, kv
+    assert (np.abs(host(out).reshape(want.shape) - want) <= c.bound(want, mag, smax, count)).all()
+    pool.release(forks)
+    assert pool.free_pages == free
