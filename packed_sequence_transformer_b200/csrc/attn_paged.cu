@@ -29,12 +29,17 @@
 // workspace; the last of the blocks to arrive, counted per (unit, head), adds
 // them in block order, so the result does not depend on who was last.
 //
-// What bounds it: reading the pages, at 90 to 96% of the rate of a plain copy
-// when there are enough (250 users, one token each over 8,000: 2.05 GB in 333 to
-// 346 us); with a window of 1,000 the same users take 61 us (258 MB, 65%), the parts'
-// beginnings and ends beside it; one user's token over 1,000: 11 us, two launches,
-// a page or two and one exchange of parts.  The fp32 build: 27 us for 5 new tokens
-// of 60 users over 700 (44 MB, 25%), its products twice as many on half the warps.
+// What bounds it (device time, cold L2): reading the pages, at 90% of the rate of a
+// plain copy when there are enough (250 users, one token each over 8,000: 2.05 GB in
+// 346 us); with a window of 1,000 the same users take 61 us (258 MB, 65%): 60 to 1,000
+// such users take 18 us and their bytes at 5.2 TB/s, for their units have 17 pages
+// where the long ones, read at 5.9 TB/s, have 125; one user's token over 1,000: 11 us,
+// two launches, a page or two and one exchange of parts.  8 new tokens of each of 60
+// users over 2,000 take 47 us, 9 or 16 take 60, 32 take 98: each further group of 8
+// reads and converts the pages again.  The fp32 build: 27 us for 5 new tokens of 60
+// users over 700 (44 MB, 25%), its products twice as many on half the warps; made for
+// few new tokens, it takes many as well: 376 us for 100 of each of 60 users over 2,000,
+// 1.06 ms for 31 prompts of 1,419 (their exponentials alone 56 us).
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -56,13 +61,13 @@ constexpr int PA_QG = 8;        // queries of a unit
 // near there.  One user over 8,000: one query 28 us, with 128 parts 46; eight
 // queries 50 us, with 128 parts 153.
 constexpr float PA_PARTS_ONE = 4.f, PA_PARTS = 1.5f;
-// 4 KB tiles in a warp's ring, about 190 KB an SM: two blocks of the bf16 build,
-// one of the fp32 build, whose two-part operands need the registers of both
-// (with two blocks it spilled: 36 us instead of 26 for 5 new tokens of 60 users
-// over 700).
 // The largest weight of a query is 2^PA_TOP, so that fp16 holds weights down to
 // 2^-39 of it (with 1 for the largest, all below 2^-25 were lost, however many).
 constexpr float PA_TOP = 15.f, PA_DOWN = 1.f / 32768.f;
+// 4 KB tiles in a warp's ring, about 190 KB an SM: two blocks of the bf16 build,
+// one of the fp32 build, whose two-part operands need the registers of both
+// (with two blocks it spilled: 36 us instead of 27 for 5 new tokens of 60 users
+// over 700).
 template <int SPLIT>
 constexpr int PA_STAGES = SPLIT == 1 ? 3 : 6;
 template <int SPLIT>

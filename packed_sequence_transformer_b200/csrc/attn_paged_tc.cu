@@ -35,9 +35,9 @@
 // cycles, of which the exponentials fill 2,048 and the products 1,250; with the
 // conversions, the exponentials, the maximum or three quarters of the products
 // left out it is at most 7% shorter each, with all of the softmax left out 50%.
-// Measured: 16 users with 256 new tokens over 16,000: 244 us, 554 TFLOP/s; 100 of
-// each of 60 users over 2,000: 103 us; 31 users' prompts of 1,419 tokens (44,000
-// in all): 207 us; a call that only begins and ends, 25 us.
+// Measured (device time, cold L2): 16 users with 256 new tokens over 16,000: 244 us,
+// 554 TFLOP/s; 100 of each of 60 users over 2,000: 100 us; 31 users' prompts of 1,419
+// tokens (44,000 in all): 208 us; a call that only begins and ends, 25 us.
 //
 // Exponent: t = s q_row k_page + log2(v_page), w = 2^(t - m): the value scale,
 // a power of two, rides in the exponent, so that O accumulates over pages in
@@ -71,9 +71,10 @@ constexpr int PTC_CONV0 = 4 * PTC_GROUPS, PTC_ISSUE0 = PTC_CONV0 + 4;  // first 
 constexpr int PTC_THREADS = 32 * (PTC_ISSUE0 + PTC_GROUPS);
 constexpr int PTC_PARTS = 16;   // units in the plan's ring: converters ask for pages up to 4 units ahead
 // 24 warps, 80 registers each at launch, dealt out anew (6 * 80 = 4 * 88 + 88 +
-// 40): with 80 everywhere the loops spill, and a spilled register costs a trip
+// 40): with 80 everywhere the loops spill more, and a spilled register costs a trip
 // to L2 here, for shared memory takes nearly all of L1 (168 us instead of 160
-// for 256 queries over each of 16 histories of 8,000 tokens).
+// for 256 queries over each of 16 histories of 8,000 tokens).  What is left spilled is
+// 12 bytes of stores and 24 of loads.
 constexpr int PTC_REGS = 88, PTC_REGS_ISSUE = 40;
 // Converted pages (keys and values of one head).  An even number: a stage then
 // belongs to one converter pair, whose order keeps its phases apart (a barrier's
@@ -91,8 +92,9 @@ constexpr int PTC_PART = 128 * (DH + 4);  // floats of one tile's part: O, then 
 // 2^15 at most, and fp16 holds them to 2^-35 of the largest (with weights of 1
 // for the largest, what lay 2^-25 below it was lost, as much as 2^20 tokens of it).
 constexpr float PTC_TOP = 11.f, PTC_RAISE = 4.f;
-// n, and the m of several groups, of a row that has seen nothing: below any score, and differences of two are
-// numbers (a test for -inf at each of them cost 5% of a call's time).
+// n, and the m of several groups, of a row that has seen nothing: below any score,
+// and differences of two are numbers (a test for -inf at each of them cost 5% of a
+// call's time).
 constexpr float PTC_NONE = -3e38f;
 
 __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) {

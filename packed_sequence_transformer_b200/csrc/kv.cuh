@@ -23,9 +23,9 @@ constexpr int KV_MIN_EXP = -100;            // smallest scale 2^-100
 // Users with at most this many new tokens take attn_paged.cu's kernel, which
 // reads the pages once for each 8 of them; the tcgen05 kernel reads them once
 // for 256, but works on 128 rows whether or not they are there.  Of 60 users
-// over 2,000 tokens each: 32 new ones 96 to 107 us in the first (25 us a group
-// of 8), 33 take 99 in the second.  The fp32 build has the first kernel only:
-// fp16 operands hold no fp32 query in one part.
+// over 2,000 tokens each: 8, 16 and 32 new ones 47, 61 and 98 us in the first, 33
+// take 94 in the second.  The fp32 build has the first kernel only, which holds
+// queries and weights in two halves each; the second has them in one.
 constexpr int PAGED_FEW = 32;
 constexpr int PAGED_FEW_STEPS = 1000, PAGED_FEW_NEW = 1024;
 constexpr int PAGED_TC_MAX_CTAS = 148;
@@ -52,7 +52,7 @@ struct PagedArgs {
   int32_t* counters;  // [CTA][head] parts of a split unit done so far
   float* partial;     // [2 CTA + which][head] unfinished sums of split units
   int num_pages, max_pages, U, T, window, sinks;
-  int few;            // users with more new tokens go to the tcgen05 kernel
+  int few;            // users with more new tokens are the tcgen05 kernel's, unless paged_all_few
 };
 
 // One user's place in a call, checked: n new tokens behind `past` kept ones.

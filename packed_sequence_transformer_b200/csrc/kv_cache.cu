@@ -50,11 +50,14 @@ int launch_kv_clear(void* ws, size_t bytes, cudaStream_t st) {
 // thread and a scan), which costs it a microsecond and saves a launch.  Block 0
 // only checks: it alone writes the error word, once, so that no launch before
 // this one has to clear it.
-// Measured: 60 users, one token each 8.8 us (launch, look-up and one item's
-// latency); 6,823 tokens 13.9 us; 44,000 tokens, 135 MB moved, 40.5 us (with whole
-// blocks of 4 heads an item, 44): five rounds of load, convert and store with 32
-// warps an SM; more would have to do with 48 registers, which spills (43 us
-// where this takes 37).
+// Measured (device time, cold L2): 60 users, one token each 8.4 us (launch, look-up
+// and one item's latency); 6,823 tokens in fp32 13.8 us; 44,000 tokens in bf16, 135 MB
+// moved, 40.4 us (with whole blocks of 4 heads an item, 44): five rounds of load,
+// convert and store with 32 warps an SM; more warps with this share of a tile each
+// would have to do with 48 registers, which spills (43 us where this takes 37 in a tight
+// loop).  The fp32 build has 16 warps an SM, whose 64 registers of input leave it
+// a 72-byte stack (88 bytes of spill stores, 92 of loads).  Four warps a tile, with
+// half the input each, were not tried.
 constexpr int KVA_THREADS = 256;
 constexpr int KVA_PAIRS = KVA_THREADS / 64;
 
@@ -348,9 +351,9 @@ int launch_kv_append(const KvAppendArgs& a, ptl_dtype dt, cudaStream_t st) {
 // -------------------------------------------------------------- page copy
 // Page dst[i] becomes a copy of page src[i], codes and scales.  A block moves a
 // quarter of a page (16 KB) at a time, four 16-byte loads of each thread in
-// flight before the first store.  3,333 pages (437 MB read and written): 75 us
-// of kernel, 5.8 TB/s, as fast as copies through shared memory; with 8 blocks
-// an SM instead of up to 32 it is 79.  Block 0 checks all page numbers and
+// flight before the first store.  3,333 pages (437 MB read and written): 70 us,
+// 6.27 TB/s, 95% of a plain copy's rate; with 8 blocks an SM instead of up to 32
+// it took 5% longer.  Block 0 checks all page numbers and
 // alone writes the error word.
 constexpr int KVC_THREADS = 256;
 constexpr int KVC_PARTS = KV_PAGE_BYTES / (KVC_THREADS * 64);
