@@ -96,10 +96,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ uint32_t pack_rest2(float lo, float hi, uint32_t first) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&first));
   return pack_half2(lo - f.x, hi - f.y);

@@ -157,10 +157,6 @@ __device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity) {
     if ((i & 63) == 0 && __any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs)) return false;
   }
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // One unit and the pages of it that this block has.  Costs (paged_tc_user_cost),
 // not pages, are laid end to end.  A page belongs to the block that its first
@@ -549,7 +545,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
           uint32_t h[4];
 #pragma unroll
           for (int b = 0; b < 4; ++b)
-            h[b] = pack_f16x2(__uint_as_float(e[b] << 16) * f, __uint_as_float(e[b] & 0xFFFF0000u) * f);
+            h[b] = pack_half2(__uint_as_float(e[b] << 16) * f, __uint_as_float(e[b] & 0xFFFF0000u) * f);
           st_shared_v4(dst + 16 * (c ^ (row & 7)), h[0], h[1], h[2], h[3]);
         }
       }
@@ -815,7 +811,7 @@ __global__ void __launch_bounds__(PTC_THREADS, 1) attn_paged_tc_kernel(const Pag
             w0 = ex2_approx(w0);
             w1 = ex2_approx(w1);
             sum[(e >> 1) & 1] = f2_add(sum[(e >> 1) & 1], f2_pack(w0, w1));
-            pk[e >> 1] = pack_f16x2(w0, w1);
+            pk[e >> 1] = pack_half2(w0, w1);
           }
           tmem_st16(tS + 16 * h, pk);  // over scores that have been read
         }

@@ -10,6 +10,7 @@
 // happens for every token served; it is paid once, in the append.
 #pragma once
 #include <cstdint>
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 
@@ -152,6 +153,11 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t codes) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
   return r;
+}
+// Two numbers to halves, lo in the low bits.
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 // 0x80 in each byte that holds a NaN code
 __device__ __forceinline__ uint32_t e4m3_nan_bytes(uint32_t w) {
