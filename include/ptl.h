@@ -507,7 +507,8 @@ ptl_status ptl_partition_users(const int32_t* cu_seqlens, int32_t num_users, int
  * users of one call, and release them.
  * Sums are held in fp32, relative to the largest weight of a row; the weights of
  * the values are rounded to fp16 in the bf16 build (to two halves, 22 bits, in the
- * fp32 build).  The sum of |value| over the keys that a query sees must stay below
+ * fp32 build), and those below 2^-35 of the row's largest may count as 0 there.
+ * The sum of |value| over the keys that a query sees must stay below
  * 2^127.  PTL_ERR_BAD_MASK for sinks < 0.  workspace:
  * ptl_attention_paged_workspace_size(T, U, dt) bytes (21 MB, whatever T, U and dt
  * are).  The error word is that of the last call with this workspace: append and

@@ -82,3 +82,34 @@ def test_values_all_of_one_size(new, exp):
     tol = BF16_HALF + FP16_HALF + 40 * (18 * 2.0 ** -24 + 64 * 2.0 ** -23)
     off = np.abs(got * 2.0 ** -exp - 1)
     assert (off <= tol).all(), (np.nanmax(off), got.min(), got.max())
+
+
+@pytest.mark.parametrize("new", [100, 300])
+@pytest.mark.parametrize("up", [True, False])
+def test_scores_against_values(new, up):
+    """Pages whose scores rise (or fall) by up to 2^45 while their values fall (or
+    rise) by as much: each page weighs about alike in the values' sum, a few all
+    in the normaliser.  (In the kernel for many new tokens: the other one holds
+    weights relative to the largest score and loses the light ones.)
+
+    Tolerance, relative: the output's and the weights' roundings; exponents, sums of
+    numbers below 2^7 rounded a few times, 4 * 2^-18 for numerator and normaliser
+    each, and 2^x 2^-22; 52 pages of 18 additions and 64 products."""
+    users, pages = 40, 50
+    total = pages + -(-new // 64)
+    key = torch.linspace(0.0, 4.0, total) if up else torch.linspace(4.0, 0.0, total)  # scores 8 * key
+    key = key.to(torch.float8_e4m3fn)
+    codes = np.zeros((total, 2, 8, 64, 64), np.uint8)
+    codes[:, 0] = key.view(torch.uint8).numpy()[:, None, None, None]
+    codes[:, 1] = 0x38  # 1.0
+    score = 8 * key.double().numpy()
+    exps = np.round(-score / np.log(2))
+    scales = np.ones((total, 2, 8), np.float32)
+    scales[:, 1] = (2.0 ** exps)[:, None]
+    got = _attend(codes, scales, np.tile(np.arange(total, dtype=np.int32), (users, 1)), users, new, 64 * pages)
+    pos = 64 * pages + np.arange(new)[:, None]
+    seen = np.clip(pos + 1 - 64 * np.arange(total)[None, :], 0, 64)
+    ref = (seen * np.exp(score) * 2.0 ** exps).sum(1) / (seen * np.exp(score)).sum(1)
+    tol = BF16_HALF + FP16_HALF + 2 * (4 * 2.0 ** -18 + 2.0 ** -22) + 52 * (18 * 2.0 ** -24 + 64 * 2.0 ** -23)
+    off = np.abs(got / ref[None, :, None] - 1)
+    assert (off <= tol).all(), (np.nanmax(off), tol)
